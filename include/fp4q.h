@@ -433,8 +433,50 @@ FP4Q_API int fp4q_gemm(const uint8_t* codes_a, const uint8_t* scales_a, const fl
  * ceil(rows / 128) * ceil(cols / block / 4); 0 for an empty tensor. */
 FP4Q_API size_t fp4q_mma_scales_size(int64_t rows, int64_t cols, int block);
 
+/*
+ * fp4q_f8_quantize -- 8-bit operands beside the 4-bit ones ("Diagnosing FP4
+ * inference", Methodology, keeps sensitive layers above 4 bits): E4M3 codes
+ * with one fp32 scale per 128 values.
+ *  x       bf16 [rows][cols] (device, 32-byte aligned); cols a multiple of 16
+ *          (FP4Q_ERR_SHAPE otherwise), rows any.  The last group of a row, and
+ *          the last tile row, may be short.
+ *  grain   FP4Q_F8_ROW: a scale per 1 x 128 values of a row (activations),
+ *          scales [rows][ceil(cols / 128)]; FP4Q_F8_TILE: a scale per 128 x 128
+ *          tile (weights), scales [ceil(rows / 128)][ceil(cols / 128)].
+ *  codes   out: rows*cols bytes, E4M3 (16-byte aligned).  scales: out, fp32.
+ * Per group: s = fp32(amax / 448) (1 when amax = 0); each code is the E4M3
+ * value nearest to fp32(x / s) (correctly rounded quotient, ties to even, sign
+ * kept).  Unlike the 4-bit quantizers this call defines non-finite inputs: a
+ * group holding NaN gets the scale NaN and NaN codes; one holding an infinity
+ * (and no NaN) the scale +inf, NaN codes for its infinities and zeros else.
+ */
+typedef enum {
+    FP4Q_F8_ROW = 0,
+    FP4Q_F8_TILE = 1
+} fp4q_f8_grain;
+FP4Q_API int fp4q_f8_quantize(const void* x, int64_t rows, int64_t cols, int grain, uint8_t* codes, float* scales,
+                              void* stream);
+
+/*
+ * fp4q_f8_gemm -- the matrix product of two fp4q_f8_quantize operands on the
+ * tensor cores:
+ *   y[i][j] = sum_b sA[i][b] sB[j / 128][b] sum_{k in block b} a[i][k] b[j][k],
+ * blocks of 128 along k.  A is m x k quantized by rows, B is n x k quantized by
+ * tiles (a linear layer's [out][in] weights).  The products are exact; a
+ * block's sum is accumulated in fp32 in the tensor cores, then fp32(sA sB)
+ * times it is added to an fp32 running sum by one fused multiply-add, and the
+ * result is rounded once.
+ *  codes_a, codes_b   [rows][k] E4M3, 16-byte aligned; k a multiple of 16
+ *          (FP4Q_ERR_SHAPE otherwise); m, n any, each below 2^31 - 256.
+ *  scales_a  [m][ceil(k / 128)]; scales_b  [ceil(n / 128)][ceil(k / 128)].
+ *  out_dtype  fp4q_out_dtype.  y: [m][n], row-major, overwritten.
+ * k == 0 writes zeros.  Enqueued on `stream`.
+ */
+FP4Q_API int fp4q_f8_gemm(const uint8_t* codes_a, const float* scales_a, int64_t m, const uint8_t* codes_b,
+                          const float* scales_b, int64_t n, int64_t k, int out_dtype, void* y, void* stream);
+
 /* The library's device fault word on the current device, read into
- * *fault_out: 0 normally; 1 once a kernel on the tensor cores (fp4q_gemm)
+ * *fault_out: 0 normally; 1 once a kernel on the tensor cores (fp4q_gemm, fp4q_f8_gemm)
  * gave up a bounded wait for its copies or matrix-multiply instructions
  * instead of hanging; the outputs of that call are then incomplete.  clear != 0 resets the word to 0
  * after reading it.  The pages have no counterpart: this is the library's own

@@ -9,6 +9,7 @@ library is missing, the first call raises ImportError.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -23,6 +24,7 @@ FP4Q_OK = 0
 FP4Q_SCALE_E8M0, FP4Q_SCALE_UE4M3, FP4Q_SCALE_UE5M3 = 0, 1, 2
 FP4Q_GLOBAL_NONE, FP4Q_GLOBAL_COMPUTE, FP4Q_GLOBAL_GIVEN, FP4Q_GLOBAL_FROM_AMAX = 0, 1, 2, 3
 FP4Q_OUT_BF16, FP4Q_OUT_F32 = 0, 1
+FP4Q_F8_ROW, FP4Q_F8_TILE = 0, 1
 
 _FMT_NAMES = {"e8m0": FP4Q_SCALE_E8M0, "mxfp4": FP4Q_SCALE_E8M0, "ue4m3": FP4Q_SCALE_UE4M3,
               "nvfp4": FP4Q_SCALE_UE4M3, "ue5m3": FP4Q_SCALE_UE5M3}
@@ -67,6 +69,8 @@ def _load() -> ctypes.CDLL:
         "fp4q_quantize_mma": (I, [P, I64, I64, I, I, I, I, P, P, P, P]),
         "fp4q_mma_scales_size": (ctypes.c_size_t, [I64, I64, I]),
         "fp4q_gemm": (I, [P, P, P, I64, P, P, P, I64, I64, I, P, P]),
+        "fp4q_f8_quantize": (I, [P, I64, I64, I, P, P, P]),
+        "fp4q_f8_gemm": (I, [P, P, I64, P, P, I64, I64, I, P, P]),
         "fp4q_global_scale_search": (I, [P, I64, I64, I, I, I, I, I, P, P, P, ctypes.c_size_t, P]),
         "fp4q_global_scale_search_workspace_size": (ctypes.c_size_t, []),
     }
@@ -116,6 +120,33 @@ def _need_cuda(*ts):
     for t in ts:
         if t is not None and not t.is_cuda:
             raise ValueError("fp4q tensors must live on a CUDA device")
+
+
+def _on(device, stream, *ts):
+    """Checks that every given tensor lives on `device` (a CUDA device), and
+    returns a context in which that device, and the given stream, are current:
+    what a call allocates or copies is then ordered with its kernels."""
+    if device.type != "cuda":
+        raise ValueError("fp4q tensors must live on a CUDA device")
+    for t in ts:
+        if t is not None and t.device != device:
+            raise ValueError("fp4q tensors of one call must live on one device")
+    if stream is not None:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device) if stream else torch.cuda.default_stream(device)
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _out(t: Optional[torch.Tensor], shape, dtype, device, name: str) -> torch.Tensor:
+    """A given output, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    return t
 
 
 def fp4q_version() -> int:
@@ -235,6 +266,61 @@ def fp4q_gemm(codes_a: torch.Tensor, scales_a: torch.Tensor, gscale_a: Optional[
     st = lib().fp4q_gemm(_ptr(codes_a), _ptr(scales_a), _ptr(gscale_a), m, _ptr(codes_b), _ptr(scales_b),
                          _ptr(gscale_b), n, 2 * kb, fmt, _ptr(y), _stream(stream))
     _check(st, "fp4q_gemm")
+    return y
+
+
+def fp4q_f8_quantize(x: torch.Tensor, grain="row", codes: Optional[torch.Tensor] = None,
+                     scales: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """E4M3 codes (torch.float8_e4m3fn [rows, cols]) and fp32 scales of a 2-D bf16
+    CUDA tensor: one per 1 x 128 values (grain "row", activations) or per
+    128 x 128 tile (grain "tile", weights)."""
+    if x.dtype != torch.bfloat16 or x.dim() != 2:
+        raise ValueError("x must be a 2-D bf16 tensor")
+    grain = {"row": FP4Q_F8_ROW, "tile": FP4Q_F8_TILE}[grain.lower()] if isinstance(grain, str) else int(grain)
+    dev = x.device
+    with _on(dev, stream, codes, scales):
+        x = x.contiguous()
+        rows, cols = x.shape
+        codes = _out(codes, (rows, cols), torch.float8_e4m3fn, dev, "codes")
+        scales = _out(scales, (rows if grain == FP4Q_F8_ROW else -(-rows // 128), -(-cols // 128)), torch.float32,
+                      dev, "scales")
+        st = lib().fp4q_f8_quantize(x.data_ptr(), rows, cols, grain, codes.data_ptr(), scales.data_ptr(),
+                                    torch.cuda.current_stream(dev).cuda_stream)
+    _check(st, "fp4q_f8_quantize")
+    return codes, scales
+
+
+def _f8_operand(codes, scales, by_tiles: bool, name: str) -> None:
+    """Checks an operand of fp4q_f8_gemm: codes and scales of the shapes fp4q_f8_quantize gives."""
+    if codes.dtype not in (torch.float8_e4m3fn, torch.uint8) or codes.dim() != 2:
+        raise ValueError(f"codes_{name} must be a 2-D float8_e4m3fn (or uint8) tensor")
+    rows, k = codes.shape
+    want = (-(-rows // 128) if by_tiles else rows, -(-k // 128))
+    if scales.dtype != torch.float32 or tuple(scales.shape) != want:
+        raise ValueError(f"scales_{name} must be a float32 tensor of shape {want}")
+
+
+def fp4q_f8_gemm(codes_a: torch.Tensor, scales_a: torch.Tensor, codes_b: torch.Tensor, scales_b: torch.Tensor,
+                 out_dtype: torch.dtype = torch.bfloat16, y: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """y = A B^T of two fp4q_f8_quantize operands, A [m, k] quantized by rows and B
+    [n, k] by tiles; returns y [m, n] in bf16 or fp32."""
+    _f8_operand(codes_a, scales_a, False, "a")
+    _f8_operand(codes_b, scales_b, True, "b")
+    m, k = codes_a.shape
+    n = codes_b.shape[0]
+    if codes_b.shape[1] != k:
+        raise ValueError("A and B must have the same k")
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+    dev = codes_a.device
+    with _on(dev, stream, scales_a, codes_b, scales_b, y):
+        codes_a, scales_a, codes_b, scales_b = (t.contiguous() for t in (codes_a, scales_a, codes_b, scales_b))
+        y = _out(y, (m, n), out_dtype, dev, "y")
+        st = lib().fp4q_f8_gemm(codes_a.data_ptr(), scales_a.data_ptr(), m, codes_b.data_ptr(), scales_b.data_ptr(),
+                                n, k, FP4Q_OUT_F32 if out_dtype == torch.float32 else FP4Q_OUT_BF16, y.data_ptr(),
+                                torch.cuda.current_stream(dev).cuda_stream)
+    _check(st, "fp4q_f8_gemm")
     return y
 
 

@@ -1,0 +1,317 @@
+// fp4q_f8_gemm.cu -- matrix product of two E4M3 operands with one fp32 scale
+// for each block of 128 along k:
+//   y[i][j] = sum_b sA[i][b] sB[j / 128][b] sum_{k in block b} a[i][k] b[j][k].
+//
+// The tensor cores take no fp32 scale, so the sum over one block of 128 is
+// formed in tensor memory (tcgen05.mma kind::f8f6f4, four instructions of
+// K = 32) and added, scaled, to running fp32 sums in registers:
+//   acc = fma(partial, fp32(sA sB), acc).
+//
+// A persistent grid (one CTA per SM) walks the 128 x BN tiles of y; each tile
+// walks k in blocks of 128 bytes through a ring of shared-memory stages:
+//   warp 0, one thread: TMA loads of the A and B code tiles;
+//   warp 1: tensor memory; one thread issues a block's MMAs into the next of
+//     512 / BN accumulators, so block b + 1 runs while block b is drained;
+//   warps 4-11: two groups of four, each draining half the columns: a thread
+//     owns a row of y (a lane of tensor memory) and BN / 2 columns, the scale
+//     is one number per thread and block, and pairs of columns are scaled and
+//     added by one packed fused multiply-add.
+// Every wait is bounded; a wait that runs out records the library's fault word
+// and the CTA stops its work and returns.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <cstring>
+
+#include "fp4q_device.cuh"
+#include "fp4q_launch.h"
+#include "fp4q_tc.cuh"
+#include "fp4q_tma.h"
+#include "../../include/fp4q.h"
+
+namespace fp4q {
+namespace f8gemm {
+
+constexpr int BM = 128, BK = 128;
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 32 * (4 + EPI_WARPS);       // three warpgroups: control, two epilogue groups
+constexpr int REGS_CONTROL = 40, REGS_EPI = 232;    // 128 x 40 + 256 x 232 = 384 x 168, the launch's registers
+constexpr uint32_t TMEM_COLS = 512;
+
+template <int BN>
+struct Shape {
+    static constexpr int A_BYTES = BM * BK;
+    static constexpr int STAGE_BYTES = A_BYTES + BN * BK;
+    static constexpr int NSTAGE = (208 * 1024) / STAGE_BYTES;
+    static constexpr int NBUF = (int)TMEM_COLS / BN;
+    static constexpr int SMEM_BYTES = 1024 + NSTAGE * STAGE_BYTES + 256;
+    static constexpr int HALF = BN / 2;                     // columns per epilogue group
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
+    static_assert(16 * (NSTAGE + NBUF) + 8 <= 256, "barriers");
+};
+
+struct Params {
+    CUtensorMap ta;                 // A codes [m][k] bytes, box 128 x 128
+    CUtensorMap tb;                 // B codes [n][k] bytes, box BN x 128
+    const float* sa;                // [m][kb]
+    const float* sb;                // [ceil(n / 128)][kb]
+    void* y;                        // [m][n]
+    int64_t m, n, kb;
+    int f32;
+    unsigned int* fault;
+};
+
+// Instruction descriptor: D fp32 (bits 4-5 = 1), A and B E4M3 (bits 7-9 and
+// 10-12 = 0), both K-major, N >> 3 in bits 17-22, M >> 4 in bits 24-28.
+__device__ __forceinline__ constexpr uint32_t idesc(int m, int n)
+{
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(id), "r"((uint32_t)acc)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// One thread's HALF results of row r, from column c0.
+template <int HALF>
+__device__ __forceinline__ void store_row(const Params& p, int64_t r, int64_t c0, const f32x2 (&acc)[HALF / 2])
+{
+    if (r >= p.m || c0 >= p.n) return;
+    if (p.f32) {
+        float* dst = static_cast<float*>(p.y) + r * p.n + c0;
+        if (c0 + HALF <= p.n && (reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
+#pragma unroll
+            for (int j = 0; j < HALF / 2; j += 4) {
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) upk(acc[j + i], v[2 * i], v[2 * i + 1]);
+                stg256(dst + 2 * j, as_u32(v[0]), as_u32(v[1]), as_u32(v[2]), as_u32(v[3]), as_u32(v[4]),
+                       as_u32(v[5]), as_u32(v[6]), as_u32(v[7]));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < HALF / 2; ++j) {
+                float a, b;
+                upk(acc[j], a, b);
+                if (c0 + 2 * j < p.n) dst[2 * j] = a;
+                if (c0 + 2 * j + 1 < p.n) dst[2 * j + 1] = b;
+            }
+        }
+    } else {
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.y) + r * p.n + c0;
+        if (c0 + HALF <= p.n && (reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
+#pragma unroll
+            for (int j = 0; j < HALF / 2; j += 8) {
+                uint32_t v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float a, b;
+                    upk(acc[j + i], a, b);
+                    v[i] = bf16x2(a, b);
+                }
+                stg256(dst + 2 * j, v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < HALF / 2; ++j) {
+                float a, b;
+                upk(acc[j], a, b);
+                if (c0 + 2 * j < p.n) dst[2 * j] = __float2bfloat16_rn(a);
+                if (c0 + 2 * j + 1 < p.n) dst[2 * j + 1] = __float2bfloat16_rn(b);
+            }
+        }
+    }
+}
+
+template <int BN>
+__global__ void __launch_bounds__(THREADS, 1) f8_gemm_kernel(const __grid_constant__ Params p)
+{
+    using S = Shape<BN>;
+    extern __shared__ __align__(1024) uint8_t smem_f8[];
+    const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_f8);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    const uint32_t full0 = base + S::NSTAGE * S::STAGE_BYTES, empty0 = full0 + 8u * S::NSTAGE;
+    const uint32_t afull0 = empty0 + 8u * S::NSTAGE, aempty0 = afull0 + 8u * S::NBUF;
+    const uint32_t slot = aempty0 + 8u * S::NBUF;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    const int64_t tiles_m = (p.m + BM - 1) / BM;
+    const int64_t n_tiles = tiles_m * ((p.n + BN - 1) / BN);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::NSTAGE; ++i) {
+            tc::mbar_init(full0 + 8u * i, 1u);
+            tc::mbar_init(empty0 + 8u * i, 1u);
+        }
+        for (int i = 0; i < S::NBUF; ++i) {
+            tc::mbar_init(afull0 + 8u * i, 1u);
+            tc::mbar_init(aempty0 + 8u * i, (uint32_t)EPI_WARPS);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tc::tmem_alloc(slot, TMEM_COLS);
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    uint32_t tmem;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(slot) : "memory");
+
+    // tiles in m-fastest order: a wave of CTAs shares a few B tiles and streams A from L2
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_CONTROL));
+        if (warp == 0 && lane == 0) {
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.ta)) : "memory");
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tb)) : "memory");
+            int s = 0;
+            uint32_t ph = 1;                                     // a fresh barrier's previous phase counts as completed
+            bool ok = true;
+            for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
+                const int m0 = (int)((t % tiles_m) * BM), n0 = (int)((t / tiles_m) * BN);
+                for (int kt = 0; kt < (int)p.kb; ++kt) {
+                    if (!tc::wait_phase(empty0 + 8u * s, ph, p.fault)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t st = base + (uint32_t)(s * S::STAGE_BYTES), fb = full0 + 8u * s;
+                    tc::mbar_expect_tx(fb, (uint32_t)S::STAGE_BYTES);
+                    tc::tma_load_2d(st, &p.ta, kt * BK, m0, fb);
+                    tc::tma_load_2d(st + S::A_BYTES, &p.tb, kt * BK, n0, fb);
+                    if (++s == S::NSTAGE) s = 0, ph ^= 1u;
+                }
+            }
+        } else if (warp == 1 && lane == 0) {
+            int s = 0, b = 0;
+            uint32_t ph = 0, bph = 1;
+            bool ok = true;
+            for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
+                for (int kt = 0; kt < (int)p.kb; ++kt) {
+                    if (!tc::wait_phase(aempty0 + 8u * b, bph, p.fault) || !tc::wait_phase(full0 + 8u * s, ph, p.fault)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::tc_fence_after();
+                    const uint32_t st = base + (uint32_t)(s * S::STAGE_BYTES);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f8(tmem + (uint32_t)(b * BN), tc::sw128_desc(st + 32u * kk),
+                               tc::sw128_desc(st + S::A_BYTES + 32u * kk), idesc(BM, BN), kk > 0);
+                    tc::mma_commit(empty0 + 8u * s);
+                    tc::mma_commit(afull0 + 8u * b);
+                    if (++s == S::NSTAGE) s = 0, ph ^= 1u;
+                    if (++b == S::NBUF) b = 0, bph ^= 1u;
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPI));
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        int b = 0;
+        uint32_t bph = 0;
+        bool ok = true;
+        for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
+            const int64_t r = (t % tiles_m) * BM + 32 * q + lane;
+            const int64_t c0 = (t / tiles_m) * BN + half * S::HALF;
+            const float* sa = p.sa + (r < p.m ? r : p.m - 1) * p.kb;
+            const float* sb = p.sb + ((c0 < p.n ? c0 : p.n - 1) >> 7) * p.kb;
+            f32x2 acc[S::HALF / 2];
+#pragma unroll
+            for (int j = 0; j < S::HALF / 2; ++j) acc[j] = 0ull;
+            float a1 = __ldg(sa), b1 = __ldg(sb);
+            for (int kt = 0; kt < (int)p.kb; ++kt) {
+                const float s = __fmul_rn(a1, b1);
+                const int nx = kt + 1 < (int)p.kb ? kt + 1 : kt;
+                a1 = __ldg(sa + nx);
+                b1 = __ldg(sb + nx);
+                const bool done = tc::wait_phase(afull0 + 8u * b, bph, p.fault);
+                if (!__all_sync(0xffffffffu, done)) {
+                    ok = false;
+                    break;
+                }
+                tc::tc_fence_after();
+                const f32x2 s2 = pk(s, s);
+#pragma unroll
+                for (int c = 0; c < S::HALF / 32; ++c) {
+                    uint32_t v[32];
+                    tc::tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(b * BN + half * S::HALF + 32 * c), v);
+                    if (c == S::HALF / 32 - 1) {
+                        tc::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(aempty0 + 8u * b);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        acc[16 * c + j] = fma2(pk(as_f32(v[2 * j]), as_f32(v[2 * j + 1])), s2, acc[16 * c + j]);
+                }
+                if (++b == S::NBUF) b = 0, bph ^= 1u;
+            }
+            if (ok) store_row<S::HALF>(p, r, c0, acc);
+        }
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+template <int BN>
+int launch(Params& p, const uint8_t* b, int64_t k, cudaStream_t s)
+{
+    if (!make_byte_map(&p.tb, b, p.n, k, BN)) return FP4Q_ERR_CUDA;
+    const int64_t tiles = ((p.m + BM - 1) / BM) * ((p.n + BN - 1) / BN);
+    const int grid = grid_for((const void*)f8_gemm_kernel<BN>, Shape<BN>::SMEM_BYTES, tiles, THREADS);
+    f8_gemm_kernel<BN><<<grid, THREADS, Shape<BN>::SMEM_BYTES, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? FP4Q_OK : FP4Q_ERR_CUDA;
+}
+
+}  // namespace f8gemm
+}  // namespace fp4q
+
+extern "C" int fp4q_f8_gemm(const uint8_t* codes_a, const float* scales_a, int64_t m, const uint8_t* codes_b,
+                            const float* scales_b, int64_t n, int64_t k, int out_dtype, void* y, void* stream)
+{
+    using namespace fp4q;
+    if (m < 0 || n < 0 || k < 0 || k % 16 != 0) return FP4Q_ERR_SHAPE;
+    if (m > INT32_MAX - 256 || n > INT32_MAX - 256 || k > INT32_MAX - 256) return FP4Q_ERR_SHAPE;   // tile coordinates are 32 bits
+    if (out_dtype != FP4Q_OUT_BF16 && out_dtype != FP4Q_OUT_F32) return FP4Q_ERR_UNSUPPORTED;
+    if (m == 0 || n == 0) return FP4Q_OK;
+    if (!y) return FP4Q_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(y) & (out_dtype == FP4Q_OUT_F32 ? 3u : 1u)) return FP4Q_ERR_ALIGN;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (k == 0)
+        return cudaMemsetAsync(y, 0, (size_t)m * (size_t)n * (out_dtype == FP4Q_OUT_F32 ? 4u : 2u), s) == cudaSuccess
+                   ? FP4Q_OK
+                   : FP4Q_ERR_CUDA;
+    if (!codes_a || !codes_b || !scales_a || !scales_b) return FP4Q_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(codes_a) & 15u) || (reinterpret_cast<uintptr_t>(codes_b) & 15u) ||
+        (reinterpret_cast<uintptr_t>(scales_a) & 3u) || (reinterpret_cast<uintptr_t>(scales_b) & 3u))
+        return FP4Q_ERR_ALIGN;
+    f8gemm::Params p;
+    memset(&p, 0, sizeof(p));
+    if (!make_byte_map(&p.ta, codes_a, m, k, f8gemm::BM)) return FP4Q_ERR_CUDA;
+    p.sa = scales_a;
+    p.sb = scales_b;
+    p.y = y;
+    p.m = m;
+    p.n = n;
+    p.kb = (k + 127) / 128;
+    p.f32 = out_dtype == FP4Q_OUT_F32;
+    p.fault = device_fault_word();
+    if (!p.fault) return FP4Q_ERR_CUDA;
+    if (n > 128 && ((m + 127) / 128) * ((n + 255) / 256) >= 148) return f8gemm::launch<256>(p, codes_b, k, s);
+    return f8gemm::launch<128>(p, codes_b, k, s);
+}

@@ -36,6 +36,7 @@
 #include "fp4q_device.cuh"
 #include "fp4q_launch.h"
 #include "fp4q_tc.cuh"
+#include "fp4q_tma.h"
 #include "../../include/fp4q.h"
 
 namespace fp4q {
@@ -57,7 +58,6 @@ constexpr uint32_t ACC_COL = 0;
 constexpr uint32_t SF_COL = 2 * BN;
 static_assert(SF_COL + NSTAGE * 32 <= TMEM_COLS, "tensor memory: accumulators and scale ring");
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
-constexpr uint32_t kMaxPolls = 1u << 24;
 
 struct Params {
     CUtensorMap ta;                 // A codes [m][k / 2] bytes, box 128 x 128, 128-byte swizzle
@@ -72,15 +72,6 @@ struct Params {
     int nvfp4;                      // 1: UE4M3 scales, block 16; 0: E8M0, block 32
     unsigned int* fault;
 };
-
-// K-major operand in the 128-byte swizzle layout (rows of 128 bytes, 8-row
-// groups 1024 bytes apart): start >> 4, leading offset 1, stride 1024 >> 4,
-// version 1, layout type 2 (SWIZZLE_128B).
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t a)
-{
-    return (uint64_t)((a >> 4) & 0x3fffu) | ((uint64_t)1u << 16) | ((uint64_t)(1024u >> 4) << 32) |
-           ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
-}
 
 // A 32-row x 16-byte scale atom in shared memory (no swizzle: 8-row core
 // matrices 128 bytes apart) as the source of tcgen05.cp.
@@ -122,34 +113,6 @@ __device__ __forceinline__ void mma_mxfp4(uint32_t d, uint64_t a, uint64_t b, ui
 __device__ __forceinline__ void tmem_cp_atom(uint32_t taddr, uint64_t sdesc)
 {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
-}
-
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
-{
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-                 : "memory");
-}
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
-
-// Bounded wait on an mbarrier phase; false (and the fault word set) when it runs out.
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, unsigned int* fault)
-{
-    for (uint32_t polls = 0; polls < kMaxPolls; ++polls)
-        if (tc::mbar_try_wait(bar, parity)) return true;
-    atomicExch(fault, 1u);
-    return false;
 }
 
 __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_constant__ Params p)
@@ -196,7 +159,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
             const int64_t m0 = (t / tiles_n) * BM, n0 = (t % tiles_n) * BN;
             for (int64_t kt = 0; kt < kt_n; ++kt, ++g) {
                 const int s = (int)(g % NSTAGE);
-                if (g >= NSTAGE && !wait_phase(empty0 + 8u * s, (uint32_t)(((g / NSTAGE) - 1) & 1), p.fault)) {
+                if (g >= NSTAGE && !tc::wait_phase(empty0 + 8u * s, (uint32_t)(((g / NSTAGE) - 1) & 1), p.fault)) {
                     ok = false;
                     break;
                 }
@@ -206,13 +169,13 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
                 if (atom0 + natoms > p.sf_kt) natoms = (int)(p.sf_kt - atom0);
                 const uint32_t st = base + (uint32_t)(s * STAGE_BYTES);
                 const uint32_t fb = full0 + 8u * s;
-                mbar_expect_tx(fb, (uint32_t)(A_BYTES + B_BYTES + 2 * natoms * 512));
-                tma_load_2d(st, &p.ta, (int)(kt * BKB), (int)m0, fb);
-                tma_load_2d(st + A_BYTES, &p.tb, (int)(kt * BKB), (int)n0, fb);
+                tc::mbar_expect_tx(fb, (uint32_t)(A_BYTES + B_BYTES + 2 * natoms * 512));
+                tc::tma_load_2d(st, &p.ta, (int)(kt * BKB), (int)m0, fb);
+                tc::tma_load_2d(st + A_BYTES, &p.tb, (int)(kt * BKB), (int)n0, fb);
                 const uint8_t* sa = p.sfa + (((m0 >> 7) * p.sf_kt + atom0) << 9);
                 const uint8_t* sb = p.sfb + (((n0 >> 7) * p.sf_kt + atom0) << 9);
-                bulk_load(st + A_BYTES + B_BYTES, sa, (uint32_t)natoms * 512u, fb);
-                bulk_load(st + A_BYTES + B_BYTES + SF_BYTES, sb, (uint32_t)natoms * 512u, fb);
+                tc::bulk_load(st + A_BYTES + B_BYTES, sa, (uint32_t)natoms * 512u, fb);
+                tc::bulk_load(st + A_BYTES + B_BYTES + SF_BYTES, sb, (uint32_t)natoms * 512u, fb);
             }
         }
     } else if (warp == 1 && lane == 0) {
@@ -221,11 +184,11 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
         bool ok = true;
         for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x, ++j) {
             const int ab = (int)(j & 1);
-            if (j >= 2 && !wait_phase(aempty0 + 8u * ab, (uint32_t)(((j >> 1) - 1) & 1), p.fault)) break;
+            if (j >= 2 && !tc::wait_phase(aempty0 + 8u * ab, (uint32_t)(((j >> 1) - 1) & 1), p.fault)) break;
             const uint32_t acc_col = tmem + ACC_COL + (uint32_t)(ab * BN);
             for (int64_t kt = 0; kt < kt_n; ++kt, ++g) {
                 const int s = (int)(g % NSTAGE);
-                if (!wait_phase(full0 + 8u * s, (uint32_t)((g / NSTAGE) & 1), p.fault)) {
+                if (!tc::wait_phase(full0 + 8u * s, (uint32_t)((g / NSTAGE) & 1), p.fault)) {
                     ok = false;
                     break;
                 }
@@ -242,8 +205,8 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
                     tmem_cp_atom(sf_b + 4u * a, atom_desc(st + A_BYTES + B_BYTES + SF_BYTES + 512u * a));
                 }
                 for (int kk = 0; kk < steps; ++kk) {
-                    const uint64_t da = sw128_desc(st + 32u * kk);
-                    const uint64_t db = sw128_desc(st + A_BYTES + 32u * kk);
+                    const uint64_t da = tc::sw128_desc(st + 32u * kk);
+                    const uint64_t db = tc::sw128_desc(st + A_BYTES + 32u * kk);
                     const bool acc = kt > 0 || kk > 0;
                     if (p.nvfp4) {
                         mma_nvfp4(acc_col, da, db, bs_idesc(true, 0), sf_a + 4u * kk, sf_b + 4u * kk, acc);
@@ -265,7 +228,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
         int64_t j = 0;
         for (int64_t t = blockIdx.x; t < n_tiles; t += gridDim.x, ++j) {
             const int ab = (int)(j & 1);
-            const bool done = wait_phase(afull0 + 8u * ab, (uint32_t)((j >> 1) & 1), p.fault);
+            const bool done = tc::wait_phase(afull0 + 8u * ab, (uint32_t)((j >> 1) & 1), p.fault);
             if (!__all_sync(0xffffffffu, done)) break;
             tc::tc_fence_after();
             const int64_t m0 = (t / tiles_n) * BM, n0 = (t % tiles_n) * BN;
@@ -307,13 +270,15 @@ __global__ void __launch_bounds__(THREADS, 1) fp4_gemm_kernel(const __grid_const
     }
 }
 
+}  // namespace gemm
+
 // The driver's cuTensorMapEncodeTiled, fetched once at run time (the library
 // links the runtime only).
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-EncodeTiledFn encode_fn()
+static EncodeTiledFn encode_fn()
 {
     static std::once_flag once;
     static EncodeTiledFn fn = nullptr;
@@ -328,23 +293,19 @@ EncodeTiledFn encode_fn()
     return fn;
 }
 
-// The code tiles of an operand: [rows][k / 2] bytes, boxes of 128 rows x 128
-// bytes (one 128-byte swizzle row per K stage), 128-byte swizzle.
-bool make_code_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t k)
+bool make_byte_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t row_bytes, int box_rows)
 {
     EncodeTiledFn enc = encode_fn();
-    const uint64_t inner = (uint64_t)(k / 2);
-    if (!enc || rows <= 0 || inner == 0) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)inner};
-    const cuuint32_t box[2] = {(cuuint32_t)BKB, (cuuint32_t)BM};
+    if (!enc || rows <= 0 || row_bytes <= 0) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+    const cuuint32_t box[2] = {128u, (cuuint32_t)box_rows};
     const cuuint32_t estr[2] = {1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-}  // namespace gemm
 }  // namespace fp4q
 
 extern "C" int fp4q_gemm(const uint8_t* codes_a, const uint8_t* scales_a, const float* gscale_a, int64_t m,
@@ -370,7 +331,7 @@ extern "C" int fp4q_gemm(const uint8_t* codes_a, const uint8_t* scales_a, const 
         return FP4Q_ERR_ALIGN;
     gemm::Params p;
     memset(&p, 0, sizeof(p));
-    if (!gemm::make_code_map(&p.ta, codes_a, m, k) || !gemm::make_code_map(&p.tb, codes_b, n, k))
+    if (!make_byte_map(&p.ta, codes_a, m, k / 2, gemm::BM) || !make_byte_map(&p.tb, codes_b, n, k / 2, gemm::BN))
         return FP4Q_ERR_CUDA;
     const int block = fmt == FP4Q_SCALE_UE4M3 ? 16 : 32;
     p.sfa = scales_a;

@@ -1,10 +1,12 @@
 // fp4q_tc.cuh -- primitives of the 5th-generation tensor cores (sm_100a):
 // tensor-memory allocation, tcgen05 fences, commits and loads, and the
-// mbarrier operations that order them.  Used by the block-scaled FP4 GEMM
-// consumer (fp4q_gemm.cu).
+// mbarrier operations that order them, and the bulk copies that complete on
+// them.
 #pragma once
 
 #include <cstdint>
+
+#include <cuda.h>
 
 namespace fp4q {
 namespace tc {
@@ -70,6 +72,45 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
 __device__ __forceinline__ void mbar_arrive(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// K-major operand in the 128-byte swizzle layout (rows of 128 bytes, 8-row
+// groups 1024 bytes apart): start >> 4, leading offset 1, stride 1024 >> 4,
+// version 1, layout type 2 (SWIZZLE_128B).
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t a)
+{
+    return (uint64_t)((a >> 4) & 0x3fffu) | ((uint64_t)1u << 16) | ((uint64_t)(1024u >> 4) << 32) |
+           ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+}
+
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+constexpr uint32_t kMaxPolls = 1u << 24;
+
+// Bounded wait on an mbarrier phase; false (and the fault word set) when it runs out.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, unsigned int* fault)
+{
+    for (uint32_t polls = 0; polls < kMaxPolls; ++polls)
+        if (mbar_try_wait(bar, parity)) return true;
+    atomicExch(fault, 1u);
+    return false;
 }
 
 }  // namespace tc
