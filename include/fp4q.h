@@ -475,8 +475,66 @@ FP4Q_API int fp4q_f8_quantize(const void* x, int64_t rows, int64_t cols, int gra
 FP4Q_API int fp4q_f8_gemm(const uint8_t* codes_a, const float* scales_a, int64_t m, const uint8_t* codes_b,
                           const float* scales_b, int64_t n, int64_t k, int out_dtype, void* y, void* stream);
 
+/*
+ * fp4q_moe -- a whole mixture-of-experts layer for a few tokens (decoding):
+ * router, the chosen experts' gated MLPs over quantized weights, and the
+ * weighted sum, in one kernel that reads each chosen expert's weights once
+ * ("Diagnosing FP4 inference", Methodology: weights in FP4, dequantized for the
+ * compute; the activations stay in 16 bits):
+ *   l = x router^T;  the top_k largest logits of each token (equal logits: the
+ *   lower expert first; NaN counts as the largest);
+ *   w = softmax(l) at the chosen experts, or with normalize != 0 softmax over
+ *   the chosen logits alone;
+ *   y = sum_j w_j D_j (silu(G_j x) * (U_j x)),  silu(v) = v / (1 + exp(-v)).
+ *  x        bf16 [tokens][hidden]; tokens 0 .. FP4Q_MOE_MAX_TOKENS.
+ *  router   bf16 [experts][hidden], or NULL when the choice was made elsewhere:
+ *           ids and weights are then read.  Otherwise they are written.
+ *  ids      int32 [tokens][top_k]; when read, an id outside 0 .. experts - 1
+ *           (-1, say, for an expert of another device) adds nothing, and an
+ *           expert may be chosen twice.  weights: fp32 [tokens][top_k].
+ *  fmt      FP4Q_SCALE_E8M0 (MXFP4, block 32) or FP4Q_SCALE_UE4M3 (NVFP4, block
+ *           16): codes and row-major scales of fp4q_quantize, no rotation;
+ *           FP4Q_F8_BLOCK128: those of fp4q_f8_quantize by tiles.
+ *  up       [experts][2 inter][hidden]: each expert's inter gate rows, then its
+ *           inter up rows.  down: [experts][hidden][inter].  Both as one matrix
+ *           of experts * rows rows, or quantized expert by expert.
+ *           gscale: the per-tensor scale of NVFP4, one for all experts
+ *           (gscale_stride 0) or one each (1), or NULL for 1; NULL otherwise.
+ *  y        bf16 [tokens][hidden], overwritten.
+ *  workspace  device scratch of at least fp4q_moe_workspace_size() bytes (16-byte
+ *           aligned).  Its first 64 bytes hold the counters through which the
+ *           kernel's CTAs wait for one another: zero before the first call that
+ *           uses the workspace, and left zero by every completed call (fill
+ *           them again after a call that set the device fault word).  One
+ *           workspace serves layers of any size; calls that share it must not
+ *           run at the same time.
+ * hidden and inter: multiples of 32 (128 for FP4Q_F8_BLOCK128), FP4Q_ERR_SHAPE
+ * otherwise, at most 65536; experts, top_k at most FP4Q_MOE_MAX_EXPERTS,
+ * FP4Q_MOE_MAX_TOPK and top_k at most experts: FP4Q_ERR_UNSUPPORTED.  x, y,
+ * router, codes, scales 16-byte aligned.  Logits are fp32 sums; inside the
+ * products x is exact to 2^-25 of the largest of each 32 values, h has 11
+ * significant bits, sums are fp32 in a fixed order, and y is rounded once.
+ * The launch is cooperative: one CTA on every SM.  Enqueued on `stream`.
+ */
+#define FP4Q_F8_BLOCK128 3             /* fmt of fp4q_moe: E4M3 with 128 x 128 scales */
+#define FP4Q_MOE_MAX_TOKENS 64
+#define FP4Q_MOE_MAX_TOPK 16
+#define FP4Q_MOE_MAX_EXPERTS 512
+typedef struct fp4q_moe_matrix {
+    const uint8_t* codes;
+    const void* scales;                /* bytes, or fp32 for FP4Q_F8_BLOCK128 */
+    const float* gscale;
+    int gscale_stride;
+} fp4q_moe_matrix;
+FP4Q_API int fp4q_moe(const void* x, int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k,
+                      const void* router, int normalize, int fmt, const fp4q_moe_matrix* up,
+                      const fp4q_moe_matrix* down, int32_t* ids, float* weights, void* y, void* workspace,
+                      size_t ws_bytes, void* stream);
+/* Bytes of device workspace of fp4q_moe for these sizes (0 for sizes it refuses). */
+FP4Q_API size_t fp4q_moe_workspace_size(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k);
+
 /* The library's device fault word on the current device, read into
- * *fault_out: 0 normally; 1 once a kernel on the tensor cores (fp4q_gemm, fp4q_f8_gemm)
+ * *fault_out: 0 normally; 1 once a kernel on the tensor cores (fp4q_gemm, fp4q_f8_gemm) or fp4q_moe
  * gave up a bounded wait for its copies or matrix-multiply instructions
  * instead of hanging; the outputs of that call are then incomplete.  clear != 0 resets the word to 0
  * after reading it.  The pages have no counterpart: this is the library's own

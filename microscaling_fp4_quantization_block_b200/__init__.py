@@ -25,6 +25,7 @@ FP4Q_SCALE_E8M0, FP4Q_SCALE_UE4M3, FP4Q_SCALE_UE5M3 = 0, 1, 2
 FP4Q_GLOBAL_NONE, FP4Q_GLOBAL_COMPUTE, FP4Q_GLOBAL_GIVEN, FP4Q_GLOBAL_FROM_AMAX = 0, 1, 2, 3
 FP4Q_OUT_BF16, FP4Q_OUT_F32 = 0, 1
 FP4Q_F8_ROW, FP4Q_F8_TILE = 0, 1
+FP4Q_F8_BLOCK128 = 3
 
 _FMT_NAMES = {"e8m0": FP4Q_SCALE_E8M0, "mxfp4": FP4Q_SCALE_E8M0, "ue4m3": FP4Q_SCALE_UE4M3,
               "nvfp4": FP4Q_SCALE_UE4M3, "ue5m3": FP4Q_SCALE_UE5M3}
@@ -71,6 +72,8 @@ def _load() -> ctypes.CDLL:
         "fp4q_gemm": (I, [P, P, P, I64, P, P, P, I64, I64, I, P, P]),
         "fp4q_f8_quantize": (I, [P, I64, I64, I, P, P, P]),
         "fp4q_f8_gemm": (I, [P, P, I64, P, P, I64, I64, I, P, P]),
+        "fp4q_moe": (I, [P, I64, I64, I64, I64, I64, P, I, I, P, P, P, P, P, P, SZ, P]),
+        "fp4q_moe_workspace_size": (SZ, [I64, I64, I64, I64, I64]),
         "fp4q_global_scale_search": (I, [P, I64, I64, I, I, I, I, I, P, P, P, ctypes.c_size_t, P]),
         "fp4q_global_scale_search_workspace_size": (ctypes.c_size_t, []),
     }
@@ -630,6 +633,88 @@ def fp4q_quantize_mse_dequantize_batched(xs, fmt, block: int, rot: int = 0, gmod
                                                     workspace.numel() * workspace.element_size(), _stream(stream))
     _check(st, "fp4q_quantize_mse_dequantize_batched")
     return outs
+
+
+class Fp4qMoeMatrix(ctypes.Structure):
+    """The experts' quantized matrices of fp4q_moe (include/fp4q.h: fp4q_moe_matrix)."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("gscale", ctypes.c_void_p),
+                ("gscale_stride", ctypes.c_int)]
+
+
+def fp4q_moe_workspace_size(tokens: int, hidden: int, inter: int, experts: int, top_k: int) -> int:
+    return lib().fp4q_moe_workspace_size(tokens, hidden, inter, experts, top_k)
+
+
+_MOE_FMT = {"mxfp4": (FP4Q_SCALE_E8M0, 32), "nvfp4": (FP4Q_SCALE_UE4M3, 16), "f8": (FP4Q_F8_BLOCK128, 128)}
+
+
+def _moe_matrix(w, fmt: str, rows: int, cols: int, experts: int, name: str) -> Fp4qMoeMatrix:
+    """One of fp4q_moe's matrices: (codes, scales[, gscale]) as the quantizers return
+    them for experts * rows rows (or with the experts as a leading dimension)."""
+    codes, scales, gscale = w if len(w) == 3 else (*w, None)
+    f8, block = fmt == "f8", _MOE_FMT[fmt][1]
+    if codes.dtype not in ((torch.float8_e4m3fn, torch.uint8) if f8 else (torch.uint8,)) or not codes.is_contiguous():
+        raise ValueError(f"{name} codes must be a contiguous {'float8_e4m3fn' if f8 else 'uint8'} tensor")
+    if codes.numel() * (1 if f8 else 2) != experts * rows * cols or codes.shape[-1] * (1 if f8 else 2) != cols:
+        raise ValueError(f"{name} codes must be those of [{experts} * {rows}, {cols}] values")
+    if scales.dtype != (torch.float32 if f8 else torch.uint8) or not scales.is_contiguous():
+        raise ValueError(f"{name} scales must be a contiguous {'float32' if f8 else 'uint8'} tensor")
+    if scales.numel() != experts * (-(-rows // 128) if f8 else rows) * (cols // block):
+        raise ValueError(f"{name} scales must be one per block of {block} of [{experts} * {rows}, {cols}] values")
+    if gscale is not None and (gscale.dtype != torch.float32 or gscale.numel() not in (1, experts)
+                               or not gscale.is_contiguous()):
+        raise ValueError(f"{name} gscale must be 1 or {experts} contiguous floats")
+    return Fp4qMoeMatrix(codes.data_ptr(), scales.data_ptr(), _ptr(gscale),
+                         0 if gscale is None or gscale.numel() == 1 else 1)
+
+
+def fp4q_moe(x: torch.Tensor, router: Optional[torch.Tensor], top_k: int, up, down, fmt, normalize: bool = True,
+             ids: Optional[torch.Tensor] = None, weights: Optional[torch.Tensor] = None,
+             y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None
+             ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """A mixture-of-experts layer for up to 64 tokens over quantized experts:
+    (y bf16 [tokens, hidden], ids int32 [tokens, top_k], weights float32).
+
+    up, down: (codes, scales, gscale) of fp4q_quantize (fmt "mxfp4", block 32, or
+    "nvfp4", block 16) or (codes, scales) of fp4q_f8_quantize by tiles (fmt "f8"),
+    for [experts * 2 inter, hidden] (gate rows, then up rows) and [experts *
+    hidden, inter].  router: bf16 [experts, hidden]; None reads ids and weights
+    instead.  workspace: zero-filled, fp4q_moe_workspace_size() bytes, kept by
+    callers that call often."""
+    if x.dtype != torch.bfloat16 or x.dim() != 2:
+        raise ValueError("x must be a 2-D bf16 tensor")
+    if fmt not in _MOE_FMT:
+        raise ValueError(f"fmt must be one of {sorted(_MOE_FMT)}")
+    tokens, hidden = x.shape
+    inter = down[0].shape[-1] * (1 if fmt == "f8" else 2)
+    dev = x.device
+    if router is not None:
+        if router.dtype != torch.bfloat16 or router.dim() != 2 or router.shape[1] != hidden:
+            raise ValueError("router must be a bf16 tensor [experts, hidden]")
+        experts = router.shape[0]
+    else:
+        if ids is None or weights is None:
+            raise ValueError("without a router, ids and weights must be given")
+        experts = down[0].numel() // max(1, hidden * down[0].shape[-1])
+    with _on(dev, stream, router, ids, weights, y, workspace, *up, *down):
+        x = x.contiguous()
+        router = None if router is None else router.contiguous()
+        if router is None:
+            ids, weights = ids.contiguous(), weights.contiguous()
+        u = _moe_matrix(up, fmt, 2 * inter, hidden, experts, "up")
+        d = _moe_matrix(down, fmt, hidden, inter, experts, "down")
+        ids = _out(ids, (tokens, top_k), torch.int32, dev, "ids")
+        weights = _out(weights, (tokens, top_k), torch.float32, dev, "weights")
+        y = _out(y, (tokens, hidden), torch.bfloat16, dev, "y")
+        if workspace is None:
+            workspace = torch.zeros((max(1, fp4q_moe_workspace_size(tokens, hidden, inter, experts, top_k)),),
+                                    dtype=torch.uint8, device=dev)
+        st = lib().fp4q_moe(x.data_ptr(), tokens, hidden, inter, experts, top_k, _ptr(router), 1 if normalize else 0,
+                            _MOE_FMT[fmt][0], ctypes.addressof(u), ctypes.addressof(d), ids.data_ptr(),
+                            weights.data_ptr(), y.data_ptr(), workspace.data_ptr(),
+                            workspace.numel() * workspace.element_size(), torch.cuda.current_stream(dev).cuda_stream)
+    _check(st, "fp4q_moe")
+    return y, ids, weights
 
 
 def fp4q_e2m1_encode_f32(r: torch.Tensor, packed: Optional[torch.Tensor] = None,

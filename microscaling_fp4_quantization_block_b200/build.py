@@ -17,7 +17,7 @@ OUT = os.path.join(PKG, "libfp4q.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["fp4q_api.cu", "fp4q_quantize.cu", "fp4q_quantize_e8m0.cu", "fp4q_quantize_ue4m3.cu",
            "fp4q_quantize_ue5m3.cu", "fp4q_search.cu", "fp4q_stats.cu", "fp4q_dequantize.cu", "fp4q_gemm.cu", "fp4q_gscale.cu",
-           "fp4q_f8.cu", "fp4q_f8_gemm.cu"]
+           "fp4q_f8.cu", "fp4q_f8_gemm.cu", "fp4q_moe.cu"]
 HEADERS = ["fp4q_device.cuh", "fp4q_kernels.cuh", "fp4q_launch.h", "fp4q_quantize_impl.cuh", "fp4q_tc.cuh", "fp4q_tma.h"]
 
 NVCC_FLAGS = [

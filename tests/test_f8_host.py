@@ -51,3 +51,38 @@ def test_f8_gemm_rejects_bad_arguments(L):
     assert g(A32, A32, 4, A32, A32, 8, 64, 1, A32 + 2, None) == -3
     assert g(None, None, 0, None, None, 8, 64, 0, None, None) == 0
     assert g(None, None, 4, None, None, 0, 64, 0, None, None) == 0
+
+
+def test_moe_rejects_bad_arguments(L):
+    import ctypes
+
+    import microscaling_fp4_quantization_block_b200 as m
+    mat = lambda **k: m.Fp4qMoeMatrix(**{**dict(codes=A32, scales=A32, gscale=None, gscale_stride=0), **k})
+    good = dict(x=A32, tokens=2, hidden=128, inter=128, experts=8, top_k=2, router=A32, norm=1, fmt=0, up=mat(),
+                down=mat(), ids=A32, w=A32, y=A32, ws=A32, ws_bytes=1 << 30)
+
+    def call(**k):
+        c = {**good, **k}
+        ref = lambda v: None if v is None else ctypes.addressof(v)
+        return L.fp4q_moe(c["x"], c["tokens"], c["hidden"], c["inter"], c["experts"], c["top_k"], c["router"],
+                          c["norm"], c["fmt"], ref(c["up"]), ref(c["down"]), c["ids"], c["w"], c["y"], c["ws"],
+                          c["ws_bytes"], None)
+
+    assert call(tokens=0) == 0 and call(tokens=0, x=None, ids=None, w=None, y=None, ws=None) == 0
+    for k in (dict(tokens=-1), dict(hidden=0), dict(inter=-32), dict(experts=0), dict(top_k=0), dict(hidden=48),
+              dict(inter=16), dict(fmt=3, hidden=160), dict(fmt=3, inter=64)):
+        assert call(**k) == -2, k
+    for k in (dict(tokens=65), dict(top_k=9), dict(experts=513), dict(experts=64, top_k=17), dict(hidden=65568),
+              dict(fmt=2), dict(fmt=4), dict(fmt=0, up=mat(gscale=A32)), dict(fmt=3, down=mat(gscale=A32)),
+              dict(fmt=1, up=mat(gscale=A32, gscale_stride=2))):
+        assert call(**k) == -4, k
+    for k in (dict(x=None), dict(up=None), dict(down=None), dict(ids=None), dict(w=None), dict(y=None), dict(ws=None),
+              dict(up=mat(codes=None)), dict(down=mat(scales=None))):
+        assert call(**k) == -1, k
+    for k in (dict(x=A32 + 8), dict(router=A32 + 8), dict(ids=A32 + 2), dict(w=A32 + 1), dict(y=A32 + 8),
+              dict(ws=A32 + 8), dict(up=mat(codes=A32 + 8)), dict(down=mat(scales=A32 + 4)),
+              dict(fmt=1, up=mat(gscale=A32 + 2))):
+        assert call(**k) == -3, k
+    need = L.fp4q_moe_workspace_size(2, 128, 128, 8, 2)
+    assert need > 0 and call(ws_bytes=need - 1) == -6
+    assert L.fp4q_moe_workspace_size(65, 128, 128, 8, 2) == 0

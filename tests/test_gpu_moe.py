@@ -1,0 +1,342 @@
+"""The mixture-of-experts layer (fp4q_moe) over MXFP4, NVFP4 and E4M3 experts,
+against the layer in 64 bits on the codes and scales that it reads.
+
+Bars (u = 2^-24, s(.) sums of magnitudes):
+- a logit differs from the exact one by at most d = (hidden / 32 + 8) u s(x r):
+  256 / 8 products a lane, then five additions.  The chosen experts must be the
+  top_k up to 2 d, in descending order up to 2 d; equal router rows give equal
+  logits and the lower expert.  A weight exp(l_j - l_max) / sum differs by a
+  factor of 1 + 4 d (two logits above, two below) and 2^-20 for expf and the sum.
+- gate and up: E = (hidden / 128 + 24) u s(W x) + 2^-25 s(W max32|x|): each of
+  the four quarters adds a block of 32 with one rounding, a block's own products
+  and scales take at most 16 more, four quarters 4, slack 4; x as fp16 is exact
+  to 2^-25 of the largest of its 32 values.
+- h = silu(g) u has |silu'| <= 1.1 and is held as fp16: 11 significant bits, so
+  its values lie 2^-10 of their power of two apart and rounding moves one by at
+  most half of that, 2^-11 of itself (and 2^-25 of the largest of its 32): Eh =
+  1.1 Eg (|u| + Eu) + |silu(g)| Eu + (2^-11 + 2^-20) |h| + 2^-25 max32|h|.
+- y: s(w D Eh) + (inter / 128 + 24 + top_k) u s(w D h) + half an ulp of bf16,
+  with the weights the call returned.
+"""
+import pytest
+import torch
+
+import workloads
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+GRID = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.float64)
+
+
+@pytest.fixture(scope="module")
+def fq():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    import microscaling_fp4_quantization_block_b200 as m
+    m.lib()
+    return m
+
+
+def experts_of(fq, fmt, experts, rows, cols, sigma, seed, per_expert=False):
+    """(codes, scales, gscale) of experts * rows Gaussian rows."""
+    w = workloads.gaussian_bf16(experts * rows, cols, sigma, seed, device="cuda")
+    if fmt == "f8":
+        return fq.fp4q_f8_quantize(w, "tile")
+    if fmt == "mxfp4":
+        c, s, _ = fq.fp4q_quantize(w, "mxfp4", 32)
+        return c, s, None
+    if per_expert:
+        parts = [fq.fp4q_quantize(w[e * rows:(e + 1) * rows] * (1 + e % 3), "nvfp4", 16, 0, "compute")
+                 for e in range(experts)]
+        return tuple(torch.cat([p[i] for p in parts]) for i in range(3))
+    return fq.fp4q_quantize(w, "nvfp4", 16, 0, "compute")
+
+
+def decode(w, fmt, experts):
+    """float64 [experts][rows][cols] on the CPU."""
+    codes, scales, g = (w[0], w[1], w[2] if len(w) > 2 else None)
+    if fmt == "f8":
+        v = codes.cpu().float().double()
+        s = scales.cpu().double().repeat_interleave(128, 0).repeat_interleave(128, 1)
+        return (v * s).view(experts, -1, v.shape[1])
+    c = codes.cpu()
+    n = torch.stack((c & 15, c >> 4), -1).view(c.shape[0], -1).long()
+    v = GRID[n & 7] * torch.where(n >= 8, -1.0, 1.0).double()
+    sc = scales.cpu()
+    s = torch.exp2(sc.double() - 127) if fmt == "mxfp4" else sc.view(torch.float8_e4m3fn).float().double()
+    v = (v * s.repeat_interleave(v.shape[1] // s.shape[1], 1)).view(experts, -1, v.shape[1])
+    return v if g is None else v * g.cpu().double().view(-1, 1, 1)
+
+
+def max32(v):
+    return v.abs().view(v.shape[0], -1, 32).amax(2).repeat_interleave(32, 1)
+
+
+def layer64(x, up, down, ids, weights):
+    """y, and how far a result may be from it."""
+    x, ids, w = x.cpu().double(), ids.cpu().long(), weights.cpu().double()
+    y = torch.zeros((x.shape[0], down.shape[1]), dtype=torch.float64)
+    far = torch.zeros_like(y)
+    hidden, inter, top_k = x.shape[1], down.shape[2], ids.shape[1]
+    for e in range(up.shape[0]):
+        token, slot = torch.nonzero(ids == e, as_tuple=True)
+        if not token.numel():
+            continue
+        xe, W, D, we = x[token], up[e], down[e], w[token, slot][:, None]
+        v = xe @ W.T
+        ev = (hidden / 128 + 24) * U * (xe.abs() @ W.abs().T) + 2.0 ** -25 * (max32(xe) @ W.abs().T)
+        g, u, eg, eu = v[:, :inter], v[:, inter:], ev[:, :inter], ev[:, inter:]
+        silu = g * torch.sigmoid(g)
+        h = silu * u
+        eh = 1.1 * eg * (u.abs() + eu) + silu.abs() * eu + (2.0 ** -11 + 2.0 ** -20) * h.abs() + 2.0 ** -25 * max32(h)
+        y.index_add_(0, token, (h @ D.T) * we)
+        far.index_add_(0, token, (eh @ D.abs().T + (inter / 128 + 24 + top_k) * U * ((h.abs() + eh) @ D.abs().T))
+                       * we.abs())
+    half = torch.finfo(torch.bfloat16).eps / 2
+    return y, far * (1 + half) + half * y.abs()
+
+
+def check_y(y, x, up, down, ids, weights):
+    want, tol = layer64(x, up, down, ids, weights)
+    err = (y.cpu().double() - want).abs()
+    assert bool((err <= tol).all()), float((err / tol.clamp(min=1e-300)).max())
+    # and not merely inside worst-case sums: far below them in the mean
+    assert float(err.norm()) <= 2.0 ** -8 * float(want.norm()) + 1e-30
+
+
+def check_route(ids, weights, x, router, top_k, normalize):
+    x, r = x.cpu().double(), router.cpu().double()
+    l = x @ r.T
+    d = (x.shape[1] / 32 + 8) * U * (x.abs() @ r.abs().T).amax(1, keepdim=True)
+    ids = ids.cpu().long()
+    assert bool(((ids >= 0) & (ids < r.shape[0])).all())
+    assert all(len(set(row)) == top_k for row in ids.tolist())
+    top = l.gather(1, ids)
+    best = l.sort(dim=1, descending=True).values[:, :top_k]
+    assert bool(((top - best).abs() <= 2 * d).all())
+    peak = top[:, :1]
+    below = torch.exp((top if normalize else l) - peak).sum(1, keepdim=True)
+    want = torch.exp(top - peak) / below
+    assert bool(((weights.cpu().double() - want).abs() <= want * (4 * d + 2.0 ** -20)).all())
+
+
+CASES = [(1, 8, 2, 256, 128), (3, 5, 5, 128, 384), (7, 60, 4, 1440, 160), (64, 16, 8, 512, 256), (23, 6, 3, 96, 32),
+         (64, 3, 1, 160, 416), (33, 40, 6, 1024, 544), (9, 512, 16, 128, 128), (64, 128, 8, 256, 128),
+         (2, 4, 2, 5120, 1792), (16, 8, 2, 2048, 768)]
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4", "f8"])
+@pytest.mark.parametrize("tokens,experts,top_k,hidden,inter", CASES)
+def test_layer(fq, fmt, tokens, experts, top_k, hidden, inter):
+    if fmt == "f8":
+        hidden, inter = -(-hidden // 128) * 128, -(-inter // 128) * 128
+    seed = tokens * 7 + experts * 3 + hidden
+    up = experts_of(fq, fmt, experts, 2 * inter, hidden, hidden ** -0.5, seed)
+    down = experts_of(fq, fmt, experts, hidden, inter, inter ** -0.5, seed + 1)
+    x = workloads.gaussian_bf16(tokens, hidden, 1.0, seed + 2, device="cuda")
+    router = workloads.gaussian_bf16(experts, hidden, hidden ** -0.5, seed + 3, device="cuda")
+    normalize = bool(seed % 2)
+    ws = torch.zeros((fq.fp4q_moe_workspace_size(tokens, hidden, inter, experts, top_k),), dtype=torch.uint8,
+                     device="cuda")
+    y, ids, w = fq.fp4q_moe(x, router, top_k, up, down, fmt, normalize, workspace=ws)
+    torch.cuda.synchronize()
+    assert fq.fp4q_device_fault() == 0
+    assert not ws[:64].any()
+    check_route(ids, w, x, router, top_k, normalize)
+    check_y(y, x, decode(up, fmt, experts), decode(down, fmt, experts), ids, w)
+    # the same again, over the workspace as it was left
+    y2, ids2, w2 = fq.fp4q_moe(x, router, top_k, up, down, fmt, normalize, workspace=ws)
+    assert torch.equal(y, y2) and torch.equal(ids, ids2) and torch.equal(w, w2)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4", "f8"])
+@pytest.mark.parametrize("kind", ["some gone", "all gone", "twice", "one expert"])
+def test_choices_made_elsewhere(fq, fmt, kind):
+    tokens, experts, top_k, hidden, inter = 37, 9, 4, 384, 256
+    g = torch.Generator().manual_seed(11)
+    ids = torch.randint(0, experts, (tokens, top_k), generator=g, dtype=torch.int32)
+    if kind == "some gone":
+        ids[torch.rand((tokens, top_k), generator=g) < 0.4] = -1
+        ids[5] = -1                                         # a token that has nothing left
+        ids[6, 1], ids[7, 2] = experts, 2 ** 31 - 1         # past the last expert
+    elif kind == "all gone":
+        ids.fill_(-1)
+    elif kind == "one expert":
+        ids.fill_(3)                                        # 148 pairs: ten groups, a token four times
+    w = torch.rand((tokens, top_k), generator=g)
+    up = experts_of(fq, fmt, experts, 2 * inter, hidden, 0.05, 1, per_expert=True)
+    down = experts_of(fq, fmt, experts, hidden, inter, 0.06, 2, per_expert=True)
+    x = workloads.gaussian_bf16(tokens, hidden, 1.0, 3, device="cuda")
+    y, i2, w2 = fq.fp4q_moe(x, None, top_k, up, down, fmt, ids=ids.cuda(), weights=w.cuda())
+    torch.cuda.synchronize()
+    assert torch.equal(i2.cpu(), ids) and torch.equal(w2.cpu(), w) and fq.fp4q_device_fault() == 0
+    check_y(y, x, decode(up, fmt, experts), decode(down, fmt, experts), ids, w)
+    nothing = ((ids < 0) | (ids >= experts)).all(1)
+    assert not y.cpu()[nothing].any()
+
+
+def test_equal_logits_take_the_lower_expert(fq):
+    tokens, experts, top_k, hidden, inter = 4, 70, 5, 256, 64
+    up = experts_of(fq, "nvfp4", experts, 2 * inter, hidden, 0.05, 1)
+    down = experts_of(fq, "nvfp4", experts, hidden, inter, 0.05, 2)
+    x = workloads.gaussian_bf16(tokens, hidden, 1.0, 3, device="cuda")
+    router = workloads.gaussian_bf16(1, hidden, 0.1, 4, device="cuda").repeat(experts, 1)
+    _, ids, w = fq.fp4q_moe(x, router, top_k, up, down, "nvfp4")
+    assert torch.equal(ids.cpu(), torch.arange(top_k, dtype=torch.int32).repeat(tokens, 1))
+    assert bool((w == w[0, 0]).all())
+    # zero tokens' logits tie as well; -0 and 0 do not differ
+    router[::2] *= -1
+    _, ids, _ = fq.fp4q_moe(torch.zeros_like(x), router, top_k, up, down, "nvfp4")
+    assert torch.equal(ids.cpu(), torch.arange(top_k, dtype=torch.int32).repeat(tokens, 1))
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4", "f8"])
+def test_scales_and_inputs_of_every_size(fq, fmt):
+    """Rows of x from 2^-60 to 2^60 and values within a row that span the format; weights whose scales span it."""
+    tokens, experts, hidden, inter = 12, 3, 256, 128
+    g = torch.Generator().manual_seed(5)
+    e = torch.randint(-12, 13, (2 * inter * experts, hidden // 128), generator=g).float()
+    w = torch.randn((experts * 2 * inter, hidden), generator=g) * torch.exp2(e).repeat_interleave(128, 1) * 0.01
+    if fmt == "f8":
+        up = fq.fp4q_f8_quantize(w.bfloat16().cuda(), "tile")
+    else:
+        up = fq.fp4q_quantize(w.bfloat16().cuda(), fmt, 32 if fmt == "mxfp4" else 16, 0,
+                              "none" if fmt == "mxfp4" else "compute")
+    down = experts_of(fq, fmt, experts, hidden, inter, 0.05, 2)
+    x = torch.randn((tokens, hidden), generator=g) * torch.exp2(torch.randint(-9, 10, (tokens, hidden), generator=g).float())
+    x *= torch.exp2(torch.linspace(-60, 20, tokens))[:, None]
+    x = x.bfloat16().cuda()
+    ids = torch.arange(tokens * 2, dtype=torch.int32).view(tokens, 2) % experts
+    wt = torch.rand((tokens, 2), generator=g)
+    y, _, _ = fq.fp4q_moe(x, None, 2, up, down, fmt, ids=ids.cuda(), weights=wt.cuda())
+    want, tol = layer64(x, decode(up, fmt, experts), decode(down, fmt, experts), ids, wt)
+    err = (y.cpu().double() - want).abs()
+    # products of powers far below the smallest normal fp32 value are not held: 2^-126 per value of h
+    tol += 2.0 ** -120
+    assert bool((err <= tol).all()), float((err / tol).max())
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4", "f8"])
+def test_tokens_stay_apart(fq, fmt):
+    """NaN or infinity in a token changes no other; the others' results do not depend on who else is there."""
+    tokens, experts, top_k, hidden, inter = 20, 6, 2, 256, 128
+    up = experts_of(fq, fmt, experts, 2 * inter, hidden, 0.06, 1)
+    down = experts_of(fq, fmt, experts, hidden, inter, 0.09, 2)
+    router = workloads.gaussian_bf16(experts, hidden, 0.06, 4, device="cuda")
+    x = workloads.gaussian_bf16(tokens, hidden, 1.0, 3, device="cuda")
+    y, ids, w = fq.fp4q_moe(x, router, top_k, up, down, fmt)
+    bad = x.clone()
+    bad[4, 17], bad[9, 200] = float("nan"), float("inf")
+    y2, ids2, w2 = fq.fp4q_moe(bad, router, top_k, up, down, fmt)
+    torch.cuda.synchronize()
+    keep = torch.ones(tokens, dtype=torch.bool)
+    keep[[4, 9]] = False
+    assert torch.equal(ids[keep], ids2[keep]) and torch.equal(w[keep], w2[keep])
+    assert torch.equal(y[keep], y2[keep]) and bool(torch.isnan(y2[4]).all())
+    assert bool(((ids2 >= 0) & (ids2 < experts)).all())
+    alone, _, _ = fq.fp4q_moe(x[3:4], router, top_k, up, down, fmt)
+    assert torch.equal(alone[0], y[3])
+    assert fq.fp4q_device_fault() == 0
+
+
+def test_workspace_graphs_streams_and_outputs(fq):
+    """One workspace for layers of several sizes in turn; captured calls replayed on new
+    inputs, two graphs sharing a workspace in turn; two streams at once with a
+    workspace each; strided x; given outputs, rows behind them left as they were."""
+    small = dict(tokens=3, experts=8, top_k=2, hidden=128, inter=64)
+    large = dict(tokens=40, experts=16, top_k=4, hidden=1024, inter=256)
+    made = []
+    for i, c in enumerate((small, large)):
+        up = experts_of(fq, "nvfp4", c["experts"], 2 * c["inter"], c["hidden"], c["hidden"] ** -0.5, 10 + i)
+        down = experts_of(fq, "nvfp4", c["experts"], c["hidden"], c["inter"], c["inter"] ** -0.5, 20 + i)
+        router = workloads.gaussian_bf16(c["experts"], c["hidden"], 0.05, 30 + i, device="cuda")
+        x = workloads.gaussian_bf16(c["tokens"], c["hidden"], 1.0, 40 + i, device="cuda")
+        x2 = workloads.gaussian_bf16(c["tokens"], c["hidden"], 1.0, 50 + i, device="cuda")
+        made.append((c, x, x2, (router, c["top_k"], up, down, "nvfp4")))
+    size = max(fq.fp4q_moe_workspace_size(c["tokens"], c["hidden"], c["inter"], c["experts"], c["top_k"])
+               for c, _, _, _ in made)
+    shared = torch.zeros((size,), dtype=torch.uint8, device="cuda")
+    plain = [(fq.fp4q_moe(x, *a)[0], fq.fp4q_moe(x2, *a)[0]) for _, x, x2, a in made]
+    for i in (0, 1, 0, 1, 1, 0):
+        assert torch.equal(fq.fp4q_moe(made[i][1], *made[i][3], workspace=shared)[0], plain[i][0])
+    graphs = []
+    for c, x, x2, a in made:
+        held = x.clone()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = fq.fp4q_moe(held, *a, workspace=shared)
+        graphs.append((g, held, out))
+    for turn in range(4):
+        for i in (0, 1):
+            g, held, out = graphs[i]
+            held.copy_(made[i][1 + (turn + i) % 2])
+            g.replay()
+            assert torch.equal(out[0], plain[i][(turn + i) % 2])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    spaces = [torch.zeros_like(shared), torch.zeros_like(shared)]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(6):
+        for i in (0, 1):
+            outs[i].append(fq.fp4q_moe(made[i][1], *made[i][3], workspace=spaces[i], stream=streams[i])[0])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, plain[i][0]) for i in (0, 1) for o in outs[i])
+    c, x, _, a = made[1]
+    wide = torch.zeros((c["tokens"], c["hidden"] + 24), dtype=torch.bfloat16, device="cuda")
+    wide[:, :c["hidden"]] = x
+    y = torch.full((c["tokens"] + 5, c["hidden"]), 9.0, dtype=torch.bfloat16, device="cuda")
+    fq.fp4q_moe(wide[:, :c["hidden"]], *a, y=y[:c["tokens"]])
+    assert torch.equal(y[:c["tokens"]], plain[1][0]) and bool((y[c["tokens"]:] == 9.0).all())
+    assert fq.fp4q_device_fault() == 0
+
+
+def test_run_of_the_operators_together(fq):
+    """A decoder layer's linear part as it would be used: activations quantized to 8 bits and
+    multiplied, the result through the experts, and the experts' result multiplied again."""
+    tokens, hidden, inter, experts = 24, 512, 256, 8
+    x = workloads.gaussian_bf16(tokens, hidden, 1.0, 1, device="cuda")
+    b, sb = fq.fp4q_f8_quantize(workloads.gaussian_bf16(hidden, hidden, hidden ** -0.5, 2, device="cuda"), "tile")
+    up = experts_of(fq, "f8", experts, 2 * inter, hidden, hidden ** -0.5, 3)
+    down = experts_of(fq, "f8", experts, hidden, inter, inter ** -0.5, 4)
+    router = workloads.gaussian_bf16(experts, hidden, 0.05, 5, device="cuda")
+    a, sa = fq.fp4q_f8_quantize(x)
+    m = fq.fp4q_f8_gemm(a, sa, b, sb)
+    y, ids, w = fq.fp4q_moe(m, router, 2, up, down, "f8")
+    a2, sa2 = fq.fp4q_f8_quantize(y)
+    z = fq.fp4q_f8_gemm(a2, sa2, b, sb, torch.float32)
+    torch.cuda.synchronize()
+    check_route(ids, w, m, router, 2, True)
+    check_y(y, m, decode(up, "f8", experts), decode(down, "f8", experts), ids, w)
+    wide = lambda c, s, r: c.cpu().float().double() * s.cpu().double().repeat_interleave(r, 0).repeat_interleave(128, 1)
+    want = wide(a2, sa2, 1) @ wide(b, sb, 128).T
+    mag = wide(a2, sa2, 1).abs() @ wide(b, sb, 128).abs().T
+    assert bool(((z.cpu().double() - want).abs() <= (17 + hidden / 128) * U * mag + U * want.abs()).all())
+
+
+def test_empty_and_refusals(fq):
+    experts, top_k, hidden, inter = 4, 2, 128, 128
+    up = experts_of(fq, "mxfp4", experts, 2 * inter, hidden, 0.05, 1)
+    down = experts_of(fq, "mxfp4", experts, hidden, inter, 0.05, 2)
+    router = workloads.gaussian_bf16(experts, hidden, 0.05, 3, device="cuda")
+    x = workloads.gaussian_bf16(2, hidden, 1.0, 4, device="cuda")
+    y, ids, w = fq.fp4q_moe(x[:0], router, top_k, up, down, "mxfp4")
+    assert y.shape == (0, hidden) and ids.shape == (0, top_k) and w.shape == (0, top_k)
+    many = workloads.gaussian_bf16(65, hidden, 1.0, 4, device="cuda")
+    for bad in (lambda: fq.fp4q_moe(many, router, top_k, up, down, "mxfp4"),
+                lambda: fq.fp4q_moe(x, router, 5, up, down, "mxfp4"),
+                lambda: fq.fp4q_moe(x, router, 0, up, down, "mxfp4"),
+                lambda: fq.fp4q_moe(x, router, top_k, up, down, "mxfp4",
+                                    workspace=torch.zeros((64,), dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(fq.Fp4qError):
+            bad()
+    for bad in (lambda: fq.fp4q_moe(x, router, top_k, up, down, "ue5m3"),
+                lambda: fq.fp4q_moe(x, router, top_k, up, down, "nvfp4"),
+                lambda: fq.fp4q_moe(x, None, top_k, up, down, "mxfp4"),
+                lambda: fq.fp4q_moe(x.float(), router, top_k, up, down, "mxfp4"),
+                lambda: fq.fp4q_moe(x, router[:, :64], top_k, up, down, "mxfp4"),
+                lambda: fq.fp4q_moe(x, router, top_k, (up[0][:-2], up[1]), down, "mxfp4"),
+                lambda: fq.fp4q_moe(x, router, top_k, up, (down[0], down[1][:-1]), "mxfp4"),
+                lambda: fq.fp4q_moe(x, None, top_k, up, down, "mxfp4", ids=torch.zeros((2, 2), device="cuda"),
+                                    weights=torch.zeros((2, 2), device="cuda"))):
+        with pytest.raises(ValueError):
+            bad()
