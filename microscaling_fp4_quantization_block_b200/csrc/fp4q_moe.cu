@@ -9,25 +9,29 @@
 // one CTA per SM walks a static share of (group, 64-row tile) items, a group
 // being up to 16 pairs of one expert, first of the gate/up matrices (32 rows
 // of each), then of the down matrices.  Per CTA
-//   warp 8 streams the items' weight rows through a ring of shared-memory
-//     stages (TMA tiles of 32 rows x 128 bytes, 128-byte swizzle; the rows'
-//     scale bytes by bulk copies).  It runs ahead of the layer's dependencies:
+//   warp 16 streams the items' weight rows through a ring of shared-memory
+//     stages (TMA tiles of 32 rows x 128 bytes, 128-byte swizzle), warp 17 the
+//     rows' scale bytes (16-byte cp.async: as bulk copies of 32 bytes they took
+//     45 ns each, one after the other, eight times the weights' time).  They run ahead of the layer's dependencies:
 //     the first down tiles are on their way while h is still being computed;
-//   warp 9 adds the pairs' activations to the stages, the down items' once all
-//     of h is written;
-//   warps 0-7 multiply: 4 quarters of the stage's k by 2 halves of its rows,
-//     mma.sync m16n8k16 with the weights as the 16 rows and the pairs as the 8
-//     columns; an item ends with the sum of the quarters.
+//   warps 18 and 19 add the pairs' activations to the stages, the down items'
+//     once all of h is written;
+//   warps 0-15 multiply: two sets take turns at the stages, in a set 4 quarters
+//     of the stage's k by 2 halves of its rows, mma.sync m16n8k16 with the
+//     weights as the 16 rows and the pairs as the 8 columns; an item ends with
+//     the sum of the eight slices of k.
 // The weights are widened to fp16 in registers on their way from shared memory
 // into the product; tcgen05.mma, whose operands lie in shared or tensor
 // memory, would need them written back first, and with a few columns per
 // expert the products are far below even the older instruction's rate.
 //
-// Activations enter the products as fp16 with one power of two per 32 values
-// (the largest of the 32 in [2^12, 2^13)): bf16 inputs keep every bit down to
-// 2^-25 of the largest, h keeps 11 bits where bf16 would keep 8.  Codes are
-// exact in fp16, and so are NVFP4's products code x UE4M3 scale; E8M0 and fp32
-// scales, and the powers of two, multiply the fp32 sums of 32 products.
+// Activations enter the products as fp16 under one power of two per row (the
+// row's largest value in [2^7, 2^8)): bf16 inputs keep every bit down to 2^-24
+// of the largest and are off by at most 2^-32 of it below that.  h is rounded to
+// fp16 under a power of its own per 32 values, which keeps 11 significant bits
+// where bf16 would keep 8, and brought to its row's power: exact down to 2^-21
+// of the row's largest value, off by at most 2^-24 of it below.  Codes are exact in fp16, and so are NVFP4's products code x
+// UE4M3 scale; E8M0 and fp32 scales multiply the fp32 sums of their blocks.
 //
 // Sums across k are in a fixed order and a token's pairs are added in slot
 // order, so results do not depend on timing.  The three points where all CTAs
@@ -52,15 +56,18 @@ namespace moe {
 
 constexpr int MAX_TOKENS = FP4Q_MOE_MAX_TOKENS, MAX_TOPK = FP4Q_MOE_MAX_TOPK, MAX_EXPERTS = FP4Q_MOE_MAX_EXPERTS;
 constexpr int MAX_PAIRS = MAX_TOKENS * MAX_TOPK;
-constexpr int CONSUMERS = 8;                            // warps that multiply
-constexpr int THREADS = 32 * (CONSUMERS + 2);
+constexpr int CONSUMERS = 16;                           // warps that multiply, two sets of 8
+constexpr int ACT_WARPS = 2;
+constexpr int THREADS = 32 * (CONSUMERS + 2 + ACT_WARPS);
 constexpr int GROUP = 16;                               // pairs per group, at most
 constexpr int TILE = 64;                                // rows per item: two boxes of 32
 constexpr int BOX_BYTES = 32 * 128;
-constexpr int RING_BYTES = 190 * 1024;
-constexpr int RED_BYTES = 18 * 1024;
+constexpr int SLICES = CONSUMERS / 2;                   // of k, per item
+constexpr int RING_BYTES = 172 * 1024;
+constexpr int RED_BYTES = 36 * 1024;                    // two buffers of 8 columns or one of 16
 constexpr int SMEM_BYTES = 1024 + RING_BYTES + RED_BYTES;
 constexpr int MAX_STAGES = 12;
+constexpr uint32_t NONE = 0xffffu;
 constexpr uint32_t kMaxSpins = 1u << 22;                // polls of a counter in global memory (about 1 us each)
 
 enum Fmt : int { kMx = FP4Q_SCALE_E8M0, kNv = FP4Q_SCALE_UE4M3, kF8 = FP4Q_F8_BLOCK128 };
@@ -85,27 +92,28 @@ struct Params {
     float* weights;
     uint16_t* y;                    // bf16 [tokens][hidden]
     Control* ctl;
-    float* logits;                  // [tokens][experts]
-    __half* xs;                     // [tokens][hidden]
-    float* xsc;                     // [tokens][hb]
-    __half* h;                      // [pairs][inter]
-    float* hsc;                     // [pairs][ib]
+    float* logits;                  // [slices of k][tokens][experts]
+    __half* xs;                     // [tokens][hp]: rows padded with zeros to hp values
+    float* xpow;                    // [tokens]
+    __half* h;                      // [pairs][ip]
+    float* hpow;                    // [pairs][ip / 32]
+    unsigned int* hmax;             // [pairs]: pattern of the largest finite |h|
     float* o;                       // [pairs][hidden]
     int tokens, hidden, inter, experts, top_k, normalize;
-    int hb, ib;                     // powers of two per row of xs and h, padded to a multiple of 4
+    int hp, ip;                     // hidden and inter, rounded up to 128
     unsigned int* fault;
 };
 
 struct Plan {                       // what the CTA knows once the choices are made
     int groups;                     // (expert, up to GROUP pairs)
     int widest;                     // pairs of the largest group
-    int stages, stage_bytes;
-    uint32_t scales_at, acts_at, pows_at;       // offsets within a stage
-    uint32_t act_pitch;
+    int stages;                     // an even number: a slot of the ring belongs to one set of warps
+    uint32_t aux_bytes, acts_at, pows_at;       // what a stage holds beside its weights: scale bytes, activations, powers
 };
 
 struct Shared {
-    int id[MAX_PAIRS];
+    uint16_t id[MAX_PAIRS];                     // NONE: no expert
+    uint16_t place[MAX_PAIRS];                  // among the pairs of its expert
     float w[MAX_PAIRS];
     uint16_t list[MAX_PAIRS];                   // pairs by expert, then by number
     uint16_t first[MAX_EXPERTS + 1];            // an expert's pairs in the list
@@ -122,12 +130,27 @@ struct Format {
     static constexpr bool f8 = FMT == kF8;
     static constexpr int CHUNKS = 2;                         // 128-byte chunks of a row per stage
     static constexpr int VALUES = CHUNKS * (f8 ? 128 : 256); // k per stage
+    static constexpr int QUARTER = VALUES / 4;               // k per warp and stage: 64 bytes of a row
     static constexpr int BLOCKS = VALUES / 32;
     static constexpr int SCALE_BYTES = FMT == kNv ? VALUES / 16 : FMT == kMx ? VALUES / 32 : 0;   // per row and stage
     static constexpr int SCALE_PITCH = SCALE_BYTES ? SCALE_BYTES + 16 : 0;
     static constexpr int ACT_PITCH = VALUES * 2 + 64;        // 64 mod 128: 16-byte reads by (pair, lane) hit all banks
-    static constexpr int POW_PITCH = BLOCKS + 4;             // floats
+    static constexpr int POW_PITCH = BLOCKS + 4;             // floats: the blocks' powers, then the row's inverse
 };
+constexpr int WEIGHT_BYTES = 2 * 2 * BOX_BYTES;              // per stage: two chunks of two boxes
+
+// Where value i of a row of activations is kept.  In the products a lane t of
+// four holds 16 bytes of a row's 64-byte quarter: 32 E2M1 values (one block, or
+// under E8M0 scales a quarter of each of four blocks) or 16 E4M3 values.  The
+// activations are stored so that the lane's 16-byte pieces j of one quarter lie
+// [j][t]: reads of one piece by the four lanes are consecutive.
+template <int FMT>
+__device__ __forceinline__ int place(int i)
+{
+    if (FMT == kNv) return (i & ~127) | ((i >> 3) & 3) << 5 | ((i >> 5) & 3) << 3 | (i & 7);
+    if (FMT == kF8) return (i & ~63) | ((i >> 3) & 1) << 5 | ((i >> 4) & 3) << 3 | (i & 7);
+    return i;
+}
 
 __device__ __forceinline__ uint32_t smem_of(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -138,7 +161,11 @@ __device__ __forceinline__ uint32_t ld_acquire(const unsigned int* p)
     return v;
 }
 
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+// Arrive on the mbarrier when this thread's cp.async copies so far have landed.
+__device__ __forceinline__ void arrive_on_copies(uint32_t bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
+}
 
 // Wait until `n` CTAs have counted; false (and the fault word set) when the wait runs out.
 __device__ bool spin(const unsigned int* counter, unsigned int n, unsigned int* fault)
@@ -151,13 +178,13 @@ __device__ bool spin(const unsigned int* counter, unsigned int n, unsigned int* 
     return false;
 }
 
-// 2^e such that the finite magnitude of fp32 pattern `bits` divided by it lies in [2^12, 2^13), and 2^-e.
+// 2^e such that the finite magnitude of fp32 pattern `bits` divided by it lies in [2^7, 2^8), and 2^-e.
 __device__ __forceinline__ void power_of(uint32_t bits, float& pow, float& inv)
 {
     int e = (int)(bits >> 23);
-    if (e < 14) e = 14;                                      // 2^-e stays finite
-    pow = as_f32((uint32_t)(e - 12) << 23);
-    inv = as_f32((uint32_t)(254 - (e - 12)) << 23);
+    if (e < 9) e = 9;                                        // 2^-e stays finite
+    pow = as_f32((uint32_t)(e - 7) << 23);
+    inv = as_f32((uint32_t)(254 - (e - 7)) << 23);
 }
 
 __device__ __forceinline__ uint32_t finite_bits(float v)
@@ -174,70 +201,98 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi)
 }
 
 // ---------------------------------------------------------------- before the products
-// x as fp16 and powers of two: four lanes per 32 values.
-__device__ void convert_x(const Params& p)
+// x as fp16 under a power of two per row: a CTA per token.
+template <int FMT>
+__device__ void convert_x(const Params& p, unsigned int* part)
 {
-    const int blocks = p.hidden / 32, total = p.tokens * blocks * 4;
-    for (int i = blockIdx.x * THREADS + threadIdx.x; i < ((total + 31) & ~31); i += gridDim.x * THREADS) {
-        const int u = i < total ? i : total - 1;             // whole warps take part in the maxima
-        const int t = u / (blocks * 4), c = (u - t * blocks * 4) * 8;
-        const uint4 w = *reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.hidden + c);
-        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-        float f[8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int i = blockIdx.x * THREADS + threadIdx.x; i < p.tokens * p.top_k; i += gridDim.x * THREADS) p.hmax[i] = 0u;
+    for (int t = blockIdx.x; t < p.tokens; t += gridDim.x) {
+        const uint16_t* x = p.x + (int64_t)t * p.hidden;
         uint32_t m = 0;
+        for (int c = threadIdx.x * 8; c < p.hidden; c += THREADS * 8) {
+            const uint4 w = *reinterpret_cast<const uint4*>(x + c);
+            const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f[2 * j] = bf16_lo(v[j]);
-            f[2 * j + 1] = bf16_hi(v[j]);
-            m = max(m, max(finite_bits(f[2 * j]), finite_bits(f[2 * j + 1])));
+            for (int j = 0; j < 4; ++j) m = max(m, max(finite_bits(bf16_lo(v[j])), finite_bits(bf16_hi(v[j]))));
         }
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0) part[warp] = m;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < THREADS / 32; ++i) m = max(m, part[i]);
         float pow, inv;
         power_of(m, pow, inv);
-        if (i < total) {
+        if (threadIdx.x == 0) p.xpow[t] = pow;
+        for (int c = threadIdx.x * 8; c < p.hp; c += THREADS * 8) {
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            if (c < p.hidden) w = *reinterpret_cast<const uint4*>(x + c);
+            const uint32_t v[4] = {w.x, w.y, w.z, w.w};
             uint32_t r[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) r[j] = f16x2(__fmul_rn(f[2 * j], inv), __fmul_rn(f[2 * j + 1], inv));
-            *reinterpret_cast<uint4*>(p.xs + (int64_t)t * p.hidden + c) = make_uint4(r[0], r[1], r[2], r[3]);
-            if ((u & 3) == 0) p.xsc[t * p.hb + c / 32] = pow;
+            for (int j = 0; j < 4; ++j) r[j] = f16x2(__fmul_rn(bf16_lo(v[j]), inv), __fmul_rn(bf16_hi(v[j]), inv));
+            *reinterpret_cast<uint4*>(p.xs + (int64_t)t * p.hp + place<FMT>(c)) = make_uint4(r[0], r[1], r[2], r[3]);
         }
+        __syncthreads();                                     // part is free again
     }
 }
 
-// Logits: a warp per (expert, up to 8 tokens), fp32 products and sums.
-__device__ void route_logits(const Params& p)
+// Slices of k that the logits are summed in, so that there is work for every
+// warp of the grid: at most 8, of at least 256 values.  The number of tokens
+// does not enter, so that a token's logits do not depend on who else is there.
+__device__ __forceinline__ int logit_slices(const Params& p)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int per = (p.tokens + 7) / 8, tasks = p.experts * per;
-    for (int task = warp * gridDim.x + blockIdx.x; task < tasks; task += gridDim.x * (THREADS / 32)) {
-        const int e = task / per, t0 = (task - e * per) * 8, nt = min(8, p.tokens - t0);
-        const uint16_t* r = p.router + (int64_t)e * p.hidden;
-        const uint16_t* x = p.x + (int64_t)t0 * p.hidden;
-        float s[8] = {};
+    return max(1, min(min(8, p.hidden / 256), (int)gridDim.x * (THREADS / 32) / p.experts));
+}
+
+// One task: expert e against N tokens from t0 (those past `last` repeat it), fp32 products and sums.
+template <int N>
+__device__ __forceinline__ void logits_of(const Params& p, int e, int t0, int from, int to, float* out)
+{
+    const int lane = threadIdx.x & 31, last = p.tokens - 1;
+    const uint16_t* r = p.router + (int64_t)e * p.hidden;
+    float s[N] = {};
 #pragma unroll 2
-        for (int c = lane * 8; c < p.hidden; c += 256) {
-            const uint4 a = *reinterpret_cast<const uint4*>(r + c);
-            const uint32_t av[4] = {a.x, a.y, a.z, a.w};
+    for (int c = from + lane * 8; c < to; c += 256) {
+        uint4 b[N];
+        const uint4 a = *reinterpret_cast<const uint4*>(r + c);
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                if (t >= nt) break;
-                const uint4 b = *reinterpret_cast<const uint4*>(x + (int64_t)t * p.hidden + c);
-                const uint32_t bv[4] = {b.x, b.y, b.z, b.w};
+        for (int t = 0; t < N; ++t) b[t] = *reinterpret_cast<const uint4*>(p.x + (int64_t)min(t0 + t, last) * p.hidden + c);
+        const uint32_t av[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    s[t] = __fmaf_rn(bf16_lo(av[j]), bf16_lo(bv[j]), s[t]);
-                    s[t] = __fmaf_rn(bf16_hi(av[j]), bf16_hi(bv[j]), s[t]);
-                }
+        for (int t = 0; t < N; ++t) {
+            const uint32_t bv[4] = {b[t].x, b[t].y, b[t].z, b[t].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[t] = __fmaf_rn(bf16_lo(av[j]), bf16_lo(bv[j]), s[t]);
+                s[t] = __fmaf_rn(bf16_hi(av[j]), bf16_hi(bv[j]), s[t]);
             }
         }
+    }
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            if (t >= nt) break;
+    for (int t = 0; t < N; ++t) {
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) s[t] += __shfl_xor_sync(0xffffffffu, s[t], d);
-            if (lane == 0) p.logits[(t0 + t) * p.experts + e] = s[t];
-        }
+        for (int d = 16; d > 0; d >>= 1) s[t] += __shfl_xor_sync(0xffffffffu, s[t], d);
+        if (lane == 0 && t0 + t <= last) out[(t0 + t) * p.experts + e] = s[t];
+    }
+}
+
+// Logits: a warp per (expert, up to 8 tokens, slice of k); the slices are added by their reader, in order.
+__device__ void route_logits(const Params& p)
+{
+    const int warp = threadIdx.x >> 5;
+    const int per = (p.tokens + 7) / 8, slices = logit_slices(p), tasks = p.experts * per * slices;
+    const int step = ((p.hidden + slices - 1) / slices + 7) & ~7;
+    for (int task = warp * gridDim.x + blockIdx.x; task < tasks; task += gridDim.x * (THREADS / 32)) {
+        const int u = task / slices, k = task - u * slices, e = u / per, t0 = (u - e * per) * 8;
+        const int from = k * step, to = min(p.hidden, from + step);
+        float* out = p.logits + (int64_t)k * p.tokens * p.experts;
+        if (p.tokens - t0 == 1)
+            logits_of<1>(p, e, t0, from, to, out);
+        else if (p.tokens - t0 <= 4)
+            logits_of<4>(p, e, t0, from, to, out);
+        else
+            logits_of<8>(p, e, t0, from, to, out);
     }
 }
 
@@ -249,69 +304,72 @@ __device__ __forceinline__ uint32_t ordered(float v)
     return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
-// The top_k experts of every token and their weights, a warp per token.
+__device__ __forceinline__ float from_ordered(uint32_t k)
+{
+    return as_f32(k == 0xffffffffu ? 0x7fc00000u : (k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+
+// The top_k experts of every token and their weights, a warp per token; a lane holds PER experts.
+template <int PER>
 __device__ void choose(const Params& p, Shared& sh)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    constexpr int PER = MAX_EXPERTS / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slices = logit_slices(p);
     for (int t = warp; t < p.tokens; t += THREADS / 32) {
-        float v[PER];
         uint32_t key[PER];
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            key[j] = 0;
             const int e = lane + 32 * j;
-            if (32 * j < p.experts && e < p.experts) {
-                v[j] = __ldcg(p.logits + t * p.experts + e);
-                key[j] = ordered(v[j]);                       // at least 0x007fffff: 0 marks what is gone
-            }
+            float part[8], v = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                part[k] = e < p.experts && k < slices ? __ldcg(p.logits + ((int64_t)k * p.tokens + t) * p.experts + e) : 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v += part[k];
+            key[j] = e < p.experts ? ordered(v) : 0u;         // an expert's is at least 0x007fffff: 0 marks what is gone
         }
-        float sum_all = 0.0f, peak = 0.0f, mine = 0.0f;
-        int chosen = -1;
-        for (int k = 0; k < p.top_k; ++k) {
-            uint32_t best = 0;
+        uint32_t best = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) best = max(best, key[j]);
+        const float peak = from_ordered(__reduce_max_sync(0xffffffffu, best));
+        float below = 0.0f;
+        if (!p.normalize) {
 #pragma unroll
             for (int j = 0; j < PER; ++j)
-                if (32 * j < p.experts) best = max(best, key[j]);
+                if (lane + 32 * j < p.experts) below += expf(from_ordered(key[j]) - peak);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) below += __shfl_xor_sync(0xffffffffu, below, d);
+        }
+        float mine = 0.0f;
+        uint32_t chosen = NONE;
+        for (int k = 0; k < p.top_k; ++k) {
             const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-            uint32_t at = 0xffffffffu;                        // the first expert that has it
+            uint32_t at = NONE;                               // the first expert that has it
 #pragma unroll
             for (int j = PER - 1; j >= 0; --j)
-                if (32 * j < p.experts && key[j] == top) at = (uint32_t)(lane + 32 * j);
+                if (key[j] == top) at = (uint32_t)(lane + 32 * j);
             at = __reduce_min_sync(0xffffffffu, at);
-            float val = 0.0f;
+            best = 0;
 #pragma unroll
-            for (int j = 0; j < PER; ++j)
-                if (32 * j < p.experts && (int)at == lane + 32 * j) {
-                    val = v[j];
-                    key[j] = 0;
-                }
-            val = __shfl_sync(0xffffffffu, val, at & 31);
-            if (k == 0) {
-                peak = val;
-                if (!p.normalize) {
-#pragma unroll
-                    for (int j = 0; j < PER; ++j)
-                        if (lane + 32 * j < p.experts) sum_all += expf(v[j] - peak);
-#pragma unroll
-                    for (int d = 16; d > 0; d >>= 1) sum_all += __shfl_xor_sync(0xffffffffu, sum_all, d);
-                }
+            for (int j = 0; j < PER; ++j) {
+                if (at == (uint32_t)(lane + 32 * j)) key[j] = 0;
+                best = max(best, key[j]);
             }
             if (lane == k) {
-                chosen = (int)at;
-                mine = expf(val - peak);
+                chosen = at;
+                mine = expf(from_ordered(top) - peak);
             }
         }
-        float below = mine;
+        if (p.normalize) {
+            below = mine;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) below += __shfl_xor_sync(0xffffffffu, below, d);
-        if (!p.normalize) below = sum_all;
+            for (int d = 16; d > 0; d >>= 1) below += __shfl_xor_sync(0xffffffffu, below, d);
+        }
         if (lane < p.top_k) {
             const float w = __fdiv_rn(mine, below);
-            sh.id[t * p.top_k + lane] = chosen;
+            sh.id[t * p.top_k + lane] = (uint16_t)chosen;
             sh.w[t * p.top_k + lane] = w;
             if (blockIdx.x == 0) {
-                p.ids[t * p.top_k + lane] = chosen;
+                p.ids[t * p.top_k + lane] = (int)chosen;
                 p.weights[t * p.top_k + lane] = w;
             }
         }
@@ -324,13 +382,21 @@ __device__ void make_plan(const Params& p, Shared& sh)
 {
     using F = Format<FMT>;
     const int pairs = p.tokens * p.top_k, lane = threadIdx.x & 31;
-    for (int e = threadIdx.x; e < p.experts; e += THREADS) {
-        int n = 0;
-        for (int i = 0; i < pairs; ++i) n += sh.id[i] == e;
-        sh.first[e + 1] = (uint16_t)n;                        // counts; summed below
-    }
+    for (int e = threadIdx.x; e <= p.experts; e += THREADS) sh.first[e] = 0;
     __syncthreads();
     if (threadIdx.x < 32) {
+        // a pair's place among its expert's, 32 pairs at a time; the counts build up in first[e + 1]
+        for (int i = lane; i < ((pairs + 31) & ~31); i += 32) {
+            const uint32_t e = i < pairs ? sh.id[i] : NONE;
+            const uint32_t same = __match_any_sync(0xffffffffu, e);
+            const int ahead = __popc(same & ((1u << lane) - 1u)), n = e != NONE ? sh.first[e + 1] : 0;
+            __syncwarp();
+            if (e != NONE) {
+                sh.place[i] = (uint16_t)(n + ahead);
+                if (ahead == 0) sh.first[e + 1] = (uint16_t)(n + __popc(same));
+            }
+            __syncwarp();
+        }
         int total = 0, groups = 0, widest = 0;
         for (int e0 = 0; e0 < p.experts; e0 += 32) {
             const int e = e0 + lane;
@@ -362,21 +428,15 @@ __device__ void make_plan(const Params& p, Shared& sh)
             Plan& q = sh.plan;
             q.groups = groups;
             q.widest = widest;
-            q.act_pitch = F::ACT_PITCH;
-            q.scales_at = F::CHUNKS * 2 * BOX_BYTES;
-            q.acts_at = q.scales_at + TILE * F::SCALE_PITCH;
-            const int columns = widest > 8 ? 16 : 8;          // what the products read; those past `widest` are not copied
-            q.pows_at = q.acts_at + columns * F::ACT_PITCH;
-            q.stage_bytes = (int)((q.pows_at + columns * F::POW_PITCH * 4 + 1023u) & ~1023u);
-            q.stages = min(MAX_STAGES, RING_BYTES / q.stage_bytes);
+            q.acts_at = TILE * F::SCALE_PITCH;
+            q.pows_at = q.acts_at + widest * F::ACT_PITCH;
+            q.aux_bytes = q.pows_at + widest * F::POW_PITCH * 4;
+            q.stages = min(MAX_STAGES, (int)(RING_BYTES / (WEIGHT_BYTES + q.aux_bytes))) & ~1;
         }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < p.experts; e += THREADS) {
-        int at = sh.first[e];
-        for (int i = 0; i < pairs; ++i)
-            if (sh.id[i] == e) sh.list[at++] = (uint16_t)i;
-    }
+    for (int i = threadIdx.x; i < pairs; i += THREADS)
+        if (sh.id[i] != NONE) sh.list[sh.first[sh.id[i]] + sh.place[i]] = (uint16_t)i;
     __syncthreads();
 }
 
@@ -419,42 +479,41 @@ __device__ __forceinline__ Phase phase_of(const Params& p, const Plan& q, int wh
     return f;
 }
 
+// The places of this CTA's stages, in order.
+struct Slots {
+    uint32_t full0, empty0;
+    int n, at;
+    uint32_t phase;
+
+    __device__ Slots(const Shared& sh)
+        : full0(smem_of(sh.full)), empty0(smem_of(sh.empty)), n(sh.plan.stages), at(0), phase(1u) {}
+    __device__ __forceinline__ bool wait_empty(unsigned int* fault) const
+    {
+        return __all_sync(0xffffffffu, tc::wait_phase(empty0 + 8u * at, phase, fault));
+    }
+    __device__ __forceinline__ void next()
+    {
+        if (++at == n) at = 0, phase ^= 1u;
+    }
+};
+
 template <int FMT>
 __device__ void stream_weights(const Params& p, const Shared& sh, uint32_t ring)
 {
     using F = Format<FMT>;
-    const int lane = threadIdx.x & 31;
-    const Plan& q = sh.plan;
-    const uint32_t full0 = smem_of(sh.full), empty0 = smem_of(sh.empty);
-    int s = 0;
-    uint32_t ph = 1;
+    Slots s(sh);
     for (int which = 0; which < 2; ++which) {
-        const Phase f = phase_of(p, q, which);
-        const int row_bytes = F::f8 ? f.k : f.k / 2, srb = FMT == kNv ? f.k / 16 : f.k / 32;
+        const Phase f = phase_of(p, sh.plan, which);
+        const int row_bytes = F::f8 ? f.k : f.k / 2;
         for (int it = f.first; it < f.items; it += gridDim.x) {
             const int g = it / f.tiles, tile = it - g * f.tiles;
             const int row0 = sh.g_expert[g] * f.rows + tile * f.step;      // experts * rows is below 2^31
-            for (int k0 = 0, b0 = 0; k0 < f.k; k0 += F::VALUES, b0 += F::CHUNKS * 128) {
-                if (!__all_sync(0xffffffffu, tc::wait_phase(empty0 + 8u * s, ph, p.fault))) return;
-                const uint32_t st = ring + (uint32_t)(s * q.stage_bytes), bar = full0 + 8u * s;
-                const int chunks = min(F::CHUNKS, (row_bytes - b0 + 127) / 128);
-                // the rows' scale bytes, widened to 16-byte boundaries (every matrix of scales ends on one)
-                int64_t src[2] = {0, 0};
-                uint32_t len[2] = {0, 0};
-                if (FMT != kF8) {
-                    const int want = min(F::SCALE_BYTES, srb - k0 / (FMT == kNv ? 16 : 32));
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int r = tile * f.step + i * f.second + lane;
-                        if (r >= f.rows) continue;                         // the second box may lie past the expert
-                        const int64_t at = (int64_t)(row0 + i * f.second + lane) * srb + k0 / (FMT == kNv ? 16 : 32);
-                        src[i] = at & ~(int64_t)15;
-                        len[i] = (uint32_t)(((at + want + 15) & ~(int64_t)15) - src[i]);
-                    }
-                }
-                const uint32_t scales = __reduce_add_sync(0xffffffffu, len[0] + len[1]);
-                if (lane == 0) {
-                    tc::mbar_expect_tx(bar, (uint32_t)(chunks * 2 * BOX_BYTES) + scales);
+            for (int b0 = 0; b0 < row_bytes; b0 += F::CHUNKS * 128) {
+                if (!s.wait_empty(p.fault)) return;
+                if ((threadIdx.x & 31) == 0) {
+                    const uint32_t st = ring + (uint32_t)(s.at * WEIGHT_BYTES), bar = s.full0 + 8u * s.at;
+                    const int chunks = min(F::CHUNKS, (row_bytes - b0 + 127) / 128);
+                    tc::mbar_expect_tx(bar, (uint32_t)(chunks * 2 * BOX_BYTES));
                     for (int c = 0; c < chunks; ++c) {
                         tc::tma_load_2d(st + (uint32_t)(c * 2 * BOX_BYTES), &f.m->map, b0 + c * 128, row0, bar);
                         tc::tma_load_2d(st + (uint32_t)(c * 2 * BOX_BYTES + BOX_BYTES), &f.m->map, b0 + c * 128,
@@ -462,58 +521,122 @@ __device__ void stream_weights(const Params& p, const Shared& sh, uint32_t ring)
                     }
                 }
                 __syncwarp();
-                if (FMT != kF8) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (len[i])
-                            tc::bulk_load(st + q.scales_at + (uint32_t)((32 * i + lane) * F::SCALE_PITCH),
-                                          static_cast<const uint8_t*>(f.m->scales) + src[i], len[i], bar);
-                }
-                if (++s == q.stages) s = 0, ph ^= 1u;
+                s.next();
             }
         }
     }
 }
 
+// The rows' scale bytes, widened to 16-byte boundaries (every matrix of scales
+// ends on one): a lane's rows and its pieces of them are the same all through
+// an item.
 template <int FMT>
-__device__ void stream_activations(const Params& p, const Shared& sh, uint32_t ring)
+__device__ void stream_scales(const Params& p, const Shared& sh, uint32_t ring)
 {
     using F = Format<FMT>;
+    constexpr int PIECES = F::SCALE_PITCH / 16, MINE = TILE * PIECES / 32;
+    const int lane = threadIdx.x & 31;
+    Slots s(sh);
+    uint32_t dst[MINE];
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
+        const int r = (lane + 32 * i) / PIECES;
+        dst[i] = (uint32_t)(r * F::SCALE_PITCH + 16 * ((lane + 32 * i) - r * PIECES));
+    }
+    for (int which = 0; which < 2; ++which) {
+        const Phase f = phase_of(p, sh.plan, which);
+        const int srb = f.k / (FMT == kNv ? 16 : 32);
+        const uint8_t* scales = static_cast<const uint8_t*>(f.m->scales);
+        for (int it = f.first; it < f.items; it += gridDim.x) {
+            const int g = it / f.tiles, tile = it - g * f.tiles;
+            const int row0 = sh.g_expert[g] * f.rows + tile * f.step;
+            const uint8_t* src[MINE];
+            int skip[MINE];                                  // row bytes that lie before the piece, less those asked for
+#pragma unroll
+            for (int i = 0; i < MINE; ++i) {
+                const int r = (lane + 32 * i) / PIECES, piece = (lane + 32 * i) - r * PIECES;
+                const int row = (r >> 5) * f.second + (r & 31);
+                const int64_t at = (int64_t)(row0 + row) * srb;
+                src[i] = scales + (at & ~(int64_t)15) + 16 * piece;
+                skip[i] = 16 * piece - (int)(at & 15);
+                if (tile * f.step + row >= f.rows) skip[i] = 1 << 30;      // the second box may lie past the expert
+            }
+            for (int from = 0; from < srb; from += F::SCALE_BYTES) {
+                if (!s.wait_empty(p.fault)) return;
+                const uint32_t aux = ring + (uint32_t)s.n * WEIGHT_BYTES + (uint32_t)s.at * sh.plan.aux_bytes;
+                const int want = min(F::SCALE_BYTES, srb - from);
+#pragma unroll
+                for (int i = 0; i < MINE; ++i) {
+                    if (skip[i] < want) cp_async16(aux + dst[i], src[i], 16u);
+                    src[i] += F::SCALE_BYTES;
+                }
+                arrive_on_copies(s.full0 + 8u * s.at);
+                s.next();
+            }
+        }
+    }
+}
+
+// The pairs' activations: pairs `mine`, mine + ACT_WARPS, ... of each group.
+template <int FMT>
+__device__ void stream_activations(const Params& p, const Shared& sh, uint32_t ring, int mine)
+{
+    using F = Format<FMT>;
+    constexpr int MOST = GROUP / ACT_WARPS, PIECES = F::VALUES / 8;        // 16-byte pieces of a pair per stage
     const int lane = threadIdx.x & 31;
     const Plan& q = sh.plan;
-    const uint32_t full0 = smem_of(sh.full), empty0 = smem_of(sh.empty);
-    int s = 0;
-    uint32_t ph = 1;
-    fence_async();                                          // x was converted by ordinary stores
+    Slots s(sh);
     for (int which = 0; which < 2; ++which) {
         const Phase f = phase_of(p, q, which);
         if (which == 1 && f.first < f.items) {
             const bool ok = spin(&p.ctl->h_done, gridDim.x, p.fault);
             if (!__all_sync(0xffffffffu, ok)) return;
-            fence_async();
         }
         const __half* acts = which == 0 ? p.xs : p.h;
-        const float* pows = which == 0 ? p.xsc : p.hsc;
-        const int pitch = which == 0 ? p.hb : p.ib;
+        const int pitch = which == 0 ? p.hp : p.ip;
         for (int it = f.first; it < f.items; it += gridDim.x) {
             const int g = it / f.tiles, n = sh.g_count[g];
-            int row = 0;
-            if (lane < n) {
-                row = sh.list[sh.g_first[g] + lane];
-                if (which == 0) row /= p.top_k;
+            const uint16_t* list = sh.list + sh.g_first[g];
+            const __half* src[MOST];
+#pragma unroll
+            for (int j = 0; j < MOST; ++j) {
+                const int c = ACT_WARPS * j + mine;
+                const int row = c < n ? (which == 0 ? list[c] / p.top_k : list[c]) : 0;
+                src[j] = acts + (int64_t)row * pitch + 8 * lane;
+            }
+            // powers of two: four lanes a pair (down items)
+            const int pc = ACT_WARPS * (lane >> 2) + mine;
+            const float* psrc = nullptr;
+            float pow, inv = 0.0f;
+            if (which == 1 && (lane >> 2) < MOST && pc < n) {
+                psrc = p.hpow + (int64_t)list[pc] * (pitch / 32) + 4 * (lane & 3);
+                power_of(__ldcg(p.hmax + list[pc]), pow, inv);
             }
             for (int k0 = 0; k0 < f.k; k0 += F::VALUES) {
-                if (!__all_sync(0xffffffffu, tc::wait_phase(empty0 + 8u * s, ph, p.fault))) return;
-                const uint32_t st = ring + (uint32_t)(s * q.stage_bytes), bar = full0 + 8u * s;
-                const int values = min(F::VALUES, f.k - k0);
-                const uint32_t ab = (uint32_t)values * 2u, pb = (uint32_t)((values / 32 + 3) & ~3) * 4u;
-                if (lane == 0) tc::mbar_expect_tx(bar, (uint32_t)n * (ab + pb));
-                __syncwarp();
-                if (lane < n) {
-                    tc::bulk_load(st + q.acts_at + (uint32_t)(lane * F::ACT_PITCH), acts + (int64_t)row * f.k + k0, ab, bar);
-                    tc::bulk_load(st + q.pows_at + (uint32_t)(lane * F::POW_PITCH * 4), pows + row * pitch + k0 / 32, pb, bar);
+                if (!s.wait_empty(p.fault)) return;
+                const uint32_t aux = ring + (uint32_t)q.stages * WEIGHT_BYTES + (uint32_t)s.at * q.aux_bytes;
+                const uint32_t bar = s.full0 + 8u * s.at, to = aux + q.acts_at + (uint32_t)(mine * F::ACT_PITCH + 16 * lane);
+                const int values = min(F::VALUES, pitch - k0);
+#pragma unroll
+                for (int j = 0; j < MOST; ++j) {
+                    if (ACT_WARPS * j + mine < n) {
+#pragma unroll
+                        for (int i = 0; i < PIECES; i += 32)
+                            if (8 * (lane + i) < values)
+                                cp_async16(to + (uint32_t)(ACT_WARPS * j * F::ACT_PITCH + 16 * i), src[j] + 8 * i, 16u);
+                    }
+                    src[j] += F::VALUES;
                 }
-                if (++s == q.stages) s = 0, ph ^= 1u;
+                if (psrc) {
+                    const uint32_t pat = aux + q.pows_at + (uint32_t)(pc * F::POW_PITCH * 4);
+                    if (128 * (lane & 3) < values) cp_async16(pat + 16u * (lane & 3), psrc + k0 / 32, 16u);
+                    if ((lane & 3) == 0)
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(pat + F::BLOCKS * 4), "f"(inv) : "memory");
+                }
+                arrive_on_copies(bar);
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(bar);         // the inverses
+                s.next();
             }
         }
     }
@@ -555,12 +678,12 @@ __device__ __forceinline__ void widen8(uint32_t lo, uint32_t hi, uint32_t (&h)[4
         : "r"(lo), "r"(hi));
 }
 
-// A UE4M3 byte as an f16 pair of equal halves.
+// Two UE4M3 bytes as f16.
 __device__ __forceinline__ uint32_t ue4m3_pair(uint32_t c)
 {
     uint32_t h;
     asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(c));
-    return __byte_perm(h, h, 0x1010);
+    return h;
 }
 
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
@@ -576,175 +699,311 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a)
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(a));
     return r;
 }
-__device__ __forceinline__ uint2 lds64(uint32_t a)
+__device__ __forceinline__ uint32_t lds16(uint32_t a)
 {
-    uint2 r;
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
-    return r;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a)
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .u8 t;\n\tld.shared.u8 t, [%1];\n\tcvt.u32.u8 %0, t;\n\t}" : "=r"(r) : "r"(a));
+    uint16_t r;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(a));
     return r;
 }
 
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * CONSUMERS) : "memory"); }
 
-// The consumer warps' part of one phase.  NT: tiles of 8 columns (pairs).
-// Within 32 values of k, lane (g, t) = (lane / 4, lane % 4) holds values
-// 8 t .. 8 t + 7 of rows g and g + 8 and of column g: the order of k inside a
-// product is free as long as both operands share it.
-template <int FMT, int NT>
-__device__ void multiply(const Params& p, const Shared& sh, uint32_t ring, float* red, int which, int& s, uint32_t& ph,
-                         bool& live)
+// A place in the CTA's sequence of stages.
+struct Cursor {
+    int slot;
+    uint32_t phase, seq;
+    bool live;
+};
+
+// One item's products: this warp's slice of k and half of the rows, acc[box][tile
+// of 8 columns].  MMA row g stands for row (g / 2) + 4 (g % 2) of 8: with the
+// 128-byte swizzle, two neighbouring g then read different halves of a row's
+// 128 bytes, and a 16-byte read by all lanes hits every bank.  The order of k
+// inside a product is free as long as both operands share it (see place).
+template <int FMT, int NT, int WHICH>
+__device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ring, uint32_t full0, uint32_t empty0,
+                                     const Phase& f, int row0, int n, Cursor& cur, float (&acc)[2][NT][4])
 {
     using F = Format<FMT>;
-    constexpr int COLS = 8 * NT, PITCH = COLS + 1;           // of the partial sums, floats
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = lane >> 2, t = lane & 3, quarter = warp & 3, half = warp >> 2;
-    const Plan& q = sh.plan;
-    const uint32_t full0 = smem_of(sh.full), empty0 = smem_of(sh.empty);
-    const Phase f = phase_of(p, q, which);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t = lane & 3, half = (warp >> 2) & 1;
+    const uint32_t set = (uint32_t)warp >> 3;
+    const int rho = (g >> 1) | ((g & 1) << 2);
     const int srb = FMT == kNv ? f.k / 16 : f.k / 32;
-    int turn = 0;
-    for (int it = f.first; it < f.items; it += gridDim.x) {
-        const int grp = it / f.tiles, tile = it - grp * f.tiles;
-        const int e = sh.g_expert[grp], n = sh.g_count[grp];
-        const int row0 = e * f.rows + tile * f.step;
-        const float* f8_scales = nullptr;                    // of this item's first box
-        int f8_second = 0;
-        if (FMT == kF8) {
-            f8_scales = static_cast<const float*>(f.m->scales) + (int64_t)(row0 >> 7) * (f.k >> 7);
-            f8_second = ((row0 + f.second) >> 7) * (f.k >> 7) - (row0 >> 7) * (f.k >> 7);
-        }
-        float acc[2][NT][4] = {};
-        for (int k0 = 0; k0 < f.k; k0 += F::VALUES) {
-            float fs[2][2];                                  // E4M3: two blocks of 128 per stage, two boxes
-            if (FMT == kF8) {
+    const float* f8_scales = nullptr;                        // of this item's first box
+    int f8_second = 0;
+    if (FMT == kF8) {
+        f8_scales = static_cast<const float*>(f.m->scales) + (int64_t)(row0 >> 7) * (f.k >> 7);
+        f8_second = ((row0 + f.second) >> 7) * (f.k >> 7) - (row0 >> 7) * (f.k >> 7);
+    }
+    int col[NT];                                             // columns past the last pair repeat it
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int kb = (k0 >> 7) + i < (f.k >> 7) ? (k0 >> 7) + i : (f.k >> 7) - 1;
-                    fs[0][i] = __ldg(f8_scales + kb);
-                    fs[1][i] = __ldg(f8_scales + f8_second + kb);
-                }
-            }
-            if (live) live = __all_sync(0xffffffffu, tc::wait_phase(full0 + 8u * s, ph, p.fault));
-            const uint32_t st = ring + (uint32_t)(s * q.stage_bytes);
-            const int blocks = min(F::BLOCKS, (f.k - k0) / 32);
-            const uint32_t w0 = st + (uint32_t)((16 * half + g) * 128);
-            uint32_t sc[2][2];                               // the scale bytes of this lane's four rows
-            if (FMT != kF8) {
-                const uint32_t at = (uint32_t)(k0 / (FMT == kNv ? 16 : 32));
+    for (int c = 0; c < NT; ++c) col[c] = min(8 * c + g, n - 1);
+
+    for (int k0 = 0; k0 < f.k; k0 += F::VALUES) {
+        const int s = cur.slot;
+        const uint32_t ph = cur.phase;
+        if (++cur.slot == q.stages) cur.slot = 0, cur.phase ^= 1u;
+        const uint32_t seq = cur.seq++;
+        if ((seq & 1u) != set) continue;
+        const int qi = (int)(((uint32_t)warp + (seq >> 1)) & 3u);      // turns, so that short stages load all alike
+        const int values = min(F::VALUES, f.k - k0);
+        float fs[2] = {};
+        if (FMT == kF8 && qi * F::QUARTER < values) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) fs[i] = __ldg(f8_scales + i * f8_second + (k0 >> 7) + (qi >> 1));
+        }
+        if (cur.live) cur.live = __all_sync(0xffffffffu, tc::wait_phase(full0 + 8u * s, ph, p.fault));
+        if (qi * F::QUARTER < values) {
+            const uint32_t aux = ring + (uint32_t)q.stages * WEIGHT_BYTES + (uint32_t)s * q.aux_bytes;
+            const uint32_t w0 = ring + (uint32_t)(s * WEIGHT_BYTES + (qi >> 1) * 2 * BOX_BYTES + (16 * half + rho) * 128);
+            const int c16 = 4 * (qi & 1);                    // of the row's 16-byte chunks, this quarter's first
+            const int left = (values - qi * F::QUARTER + 31) / 32;     // blocks of 32 in this quarter, at least
+            uint32_t act[NT];
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+                act[c] = aux + q.acts_at + (uint32_t)(col[c] * F::ACT_PITCH + qi * F::QUARTER * 2 + 16 * t);
+
+            if constexpr (FMT == kMx) {
+                // four blocks of 32; a lane holds values 8 t .. 8 t + 7 of each
+                uint32_t sc[2][2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const uint32_t row = (uint32_t)(row0 + i * f.second + 16 * half + 8 * r + g);
-                        sc[i][r] = st + q.scales_at + (uint32_t)((32 * i + 16 * half + 8 * r + g) * F::SCALE_PITCH) +
-                                   ((row * (uint32_t)srb + at) & 15u);
+                        const int row = 16 * half + 8 * r + rho;
+                        const uint32_t lead = (uint32_t)((row0 + i * f.second + row) * srb + k0 / 32) & 15u;
+                        const uint32_t at = aux + (uint32_t)((32 * i + row) * F::SCALE_PITCH) + lead + 4u * qi;
+                        // four bytes that may straddle two words (one block may follow the last: not used)
+                        const uint32_t lo = lds32(at & ~3u), hi = lds32((at & ~3u) + 4u * ((at & 3u) != 0u));
+                        sc[i][r] = __funnelshift_r(lo, hi, 8u * (at & 3u));
                     }
-            }
-            for (int b = quarter; b < blocks; b += 4) {
-                uint32_t bf[NT][4];
-                float pw[NT][2];
-#pragma unroll
-                for (int c = 0; c < NT; ++c) {
-                    const uint4 v = lds128(st + q.acts_at + (uint32_t)((8 * c + g) * F::ACT_PITCH + 64 * b + 16 * t));
-                    bf[c][0] = v.x, bf[c][1] = v.y, bf[c][2] = v.z, bf[c][3] = v.w;
-                    const uint32_t pa = st + q.pows_at + (uint32_t)(((8 * c + 2 * t) * F::POW_PITCH + b) * 4);
-                    pw[c][0] = as_f32(lds32(pa));
-                    pw[c][1] = as_f32(lds32(pa + F::POW_PITCH * 4));
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {                // the two boxes
-                    uint32_t a[2][4];
-                    float rs[2] = {1.0f, 1.0f};
-                    if (FMT == kF8) {
-                        const uint32_t wa = w0 + (uint32_t)((b >> 2) * 2 * BOX_BYTES + i * BOX_BYTES) +
-                                            ((uint32_t)((2 * (b & 3) + (t >> 1)) ^ g) << 4) + 8u * (t & 1);
-                        const uint2 v0 = lds64(wa), v1 = lds64(wa + 1024u);
-                        widen8(v0.x, v0.y, a[0]);
-                        widen8(v1.x, v1.y, a[1]);
-                        rs[0] = rs[1] = fs[i][b >> 2];
-                    } else {
-                        const uint32_t wa = w0 + (uint32_t)((b >> 3) * 2 * BOX_BYTES + i * BOX_BYTES) +
-                                            ((uint32_t)((b & 7) ^ g) << 4) + 4u * t;
-                        widen4(lds32(wa), a[0]);
-                        widen4(lds32(wa + 1024u), a[1]);
-                        if (FMT == kNv) {
-#pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                const uint32_t m = ue4m3_pair(lds8(sc[i][r] + 2u * b + (t >> 1)));
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) a[r][j] = mul_f16x2(a[r][j], m);
-                            }
-                        } else {
-                            rs[0] = e8m0_decode(lds8(sc[i][0] + b));
-                            rs[1] = e8m0_decode(lds8(sc[i][1] + b));
-                        }
-                    }
+                f32x2 ratio[NT][2];
+                if constexpr (WHICH == 1) {
 #pragma unroll
                     for (int c = 0; c < NT; ++c) {
-                        float d[4] = {};
-                        mma16(d, a[0][0], a[1][0], a[0][1], a[1][1], bf[c][0], bf[c][1]);
-                        mma16(d, a[0][2], a[1][2], a[0][3], a[1][3], bf[c][2], bf[c][3]);
+                        const uint32_t pa = aux + q.pows_at + (uint32_t)(col[c] * F::POW_PITCH * 4);
+                        const float inv = as_f32(lds32(pa + F::BLOCKS * 4));
+                        lds_pairs(pa + 16u * qi, ratio[c][0], ratio[c][1]);
+                        ratio[c][0] = mul2(ratio[c][0], pk(inv, inv));
+                        ratio[c][1] = mul2(ratio[c][1], pk(inv, inv));
+                    }
+                }
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float m = FMT == kNv ? pw[c][j & 1] : __fmul_rn(rs[j >> 1], pw[c][j & 1]);
-                            acc[i][c][j] = __fmaf_rn(d[j], m, acc[i][c][j]);
+                for (int b = 0; b < 4; ++b) {
+                    if (b >= left) break;
+                    uint4 bf[NT];
+#pragma unroll
+                    for (int c = 0; c < NT; ++c) {
+                        bf[c] = lds128(act[c] + 64u * b);
+                        if constexpr (WHICH == 1) {
+                            float r0, r1;
+                            upk(ratio[c][b >> 1], r0, r1);
+                            const uint32_t m = (b & 1) ? f16x2(r1, r1) : f16x2(r0, r0);
+                            bf[c].x = mul_f16x2(bf[c].x, m), bf[c].y = mul_f16x2(bf[c].y, m);
+                            bf[c].z = mul_f16x2(bf[c].z, m), bf[c].w = mul_f16x2(bf[c].w, m);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t wa = w0 + (uint32_t)(i * BOX_BYTES) + ((uint32_t)((c16 + b) ^ rho) << 4) + 4u * t;
+                        uint32_t a0[4], a1[4];
+                        widen4(lds32(wa), a0);
+                        widen4(lds32(wa + 1024u), a1);
+                        const float s0 = e8m0_decode((sc[i][0] >> (8 * b)) & 255u);
+                        const float s1 = e8m0_decode((sc[i][1] >> (8 * b)) & 255u);
+#pragma unroll
+                        for (int c = 0; c < NT; ++c) {
+                            float d[4] = {};
+                            mma16(d, a0[0], a1[0], a0[1], a1[1], bf[c].x, bf[c].y);
+                            mma16(d, a0[2], a1[2], a0[3], a1[3], bf[c].z, bf[c].w);
+                            float(&o)[4] = acc[i][c];
+                            upk(fma2(pk(d[0], d[1]), pk(s0, s0), pk(o[0], o[1])), o[0], o[1]);
+                            upk(fma2(pk(d[2], d[3]), pk(s1, s1), pk(o[2], o[3])), o[2], o[3]);
                         }
                     }
                 }
-            }
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(empty0 + 8u * s);
-            if (++s == q.stages) s = 0, ph ^= 1u;
-        }
-
-        // the four quarters of k, added in order
-        float* buf = red + (NT == 1 ? turn * (4 * TILE * PITCH) : 0);
-        turn ^= 1;
-        if (NT > 1) consumers_sync();                        // one buffer: the last item's readers are done
+            } else {
+                constexpr int PIECES = FMT == kNv ? 4 : 2;   // 16-byte pieces of activations per lane
+                uint4 bf[NT][PIECES];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+                for (int c = 0; c < NT; ++c) {
 #pragma unroll
-            for (int c = 0; c < NT; ++c)
+                    for (int j = 0; j < PIECES; ++j) bf[c][j] = lds128(act[c] + 64u * j);
+                    if constexpr (WHICH == 1) {
+                        const uint32_t pa = aux + q.pows_at + (uint32_t)(col[c] * F::POW_PITCH * 4);
+                        const int block = FMT == kNv ? 4 * qi + t : 2 * qi + (t >> 1);
+                        const float r = __fmul_rn(as_f32(lds32(pa + 4u * block)), as_f32(lds32(pa + F::BLOCKS * 4)));
+                        const uint32_t m = f16x2(r, r);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    buf[(quarter * TILE + 32 * i + 16 * half + g + 8 * (j >> 1)) * PITCH + 8 * c + 2 * t + (j & 1)] =
-                        acc[i][c][j];
-        consumers_sync();
-        const float gs = FMT == kNv && f.m->gscale ? __ldg(f.m->gscale + e * f.m->gstride) : 1.0f;
-        const uint16_t* list = sh.list + sh.g_first[grp];
-        if (which == 0) {
-            // a warp per pair: 32 consecutive values of h share a power of two
-            for (int c = warp; c < n; c += CONSUMERS) {
-                float a = 0.0f, b = 0.0f;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    a += buf[(k * TILE + lane) * PITCH + c];
-                    b += buf[(k * TILE + 32 + lane) * PITCH + c];
+                        for (int j = 0; j < PIECES; ++j) {
+                            bf[c][j].x = mul_f16x2(bf[c][j].x, m), bf[c][j].y = mul_f16x2(bf[c][j].y, m);
+                            bf[c][j].z = mul_f16x2(bf[c][j].z, m), bf[c][j].w = mul_f16x2(bf[c][j].w, m);
+                        }
+                    }
                 }
-                a = __fmul_rn(a, gs);
-                b = __fmul_rn(b, gs);
-                const float v = __fmul_rn(__fdiv_rn(a, 1.0f + expf(-a)), b);
-                float pow, inv;
-                power_of(__reduce_max_sync(0xffffffffu, finite_bits(v)), pow, inv);
-                const int64_t pair = list[c];
-                p.h[pair * p.inter + tile * 32 + lane] = __float2half_rn(__fmul_rn(v, inv));
-                if (lane == 0) p.hsc[pair * p.ib + tile] = pow;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t wa = w0 + (uint32_t)(i * BOX_BYTES) + ((uint32_t)((c16 + t) ^ rho) << 4);
+                    const uint4 v0 = lds128(wa), v1 = lds128(wa + 1024u);
+                    const uint32_t u0[4] = {v0.x, v0.y, v0.z, v0.w}, u1[4] = {v1.x, v1.y, v1.z, v1.w};
+                    if constexpr (FMT == kNv) {
+                        uint32_t m[2][2];                    // two scales per row and block
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const int row = 16 * half + 8 * r + rho;
+                            const uint32_t lead = (uint32_t)((row0 + i * f.second + row) * srb + k0 / 16) & 15u;
+                            const uint32_t h = ue4m3_pair(lds16(aux + (uint32_t)((32 * i + row) * F::SCALE_PITCH) + lead +
+                                                                2u * (4 * qi + t)));
+                            m[r][0] = t < left ? __byte_perm(h, h, 0x1010) : 0u;     // past the row: zeros times zeros
+                            m[r][1] = t < left ? __byte_perm(h, h, 0x3232) : 0u;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t a0[4], a1[4];
+                            widen4(u0[j], a0);
+                            widen4(u1[j], a1);
+#pragma unroll
+                            for (int l = 0; l < 4; ++l) {
+                                a0[l] = mul_f16x2(a0[l], m[0][j >> 1]);
+                                a1[l] = mul_f16x2(a1[l], m[1][j >> 1]);
+                            }
+#pragma unroll
+                            for (int c = 0; c < NT; ++c) {
+                                mma16(acc[i][c], a0[0], a1[0], a0[1], a1[1], bf[c][j].x, bf[c][j].y);
+                                mma16(acc[i][c], a0[2], a1[2], a0[3], a1[3], bf[c][j].z, bf[c][j].w);
+                            }
+                        }
+                    } else {
+                        float d[NT][4] = {};
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            uint32_t a0[4], a1[4];
+                            widen8(u0[2 * j], u0[2 * j + 1], a0);
+                            widen8(u1[2 * j], u1[2 * j + 1], a1);
+#pragma unroll
+                            for (int c = 0; c < NT; ++c) {
+                                mma16(d[c], a0[0], a1[0], a0[1], a1[1], bf[c][j].x, bf[c][j].y);
+                                mma16(d[c], a0[2], a1[2], a0[3], a1[3], bf[c][j].z, bf[c][j].w);
+                            }
+                        }
+#pragma unroll
+                        for (int c = 0; c < NT; ++c)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) acc[i][c][j] = __fmaf_rn(d[c][j], fs[i], acc[i][c][j]);
+                    }
+                }
             }
-        } else {
-            const int r = tid & (TILE - 1);
-            if (tile * TILE + r < p.hidden)
-                for (int c = tid / TILE; c < n; c += 32 * CONSUMERS / TILE) {
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(empty0 + 8u * s);
+    }
+}
+
+// An item from its products to h (WHICH 0) or to the pairs' results (1).
+template <int FMT, int NT, int WHICH>
+__device__ __forceinline__ void whole_item(const Params& p, const Shared& sh, uint32_t ring, float* buf, const Phase& f,
+                                           int it, bool wait_first, Cursor& cur)
+{
+    constexpr int PITCH = 8 * NT + 1;                        // of the partial sums, floats
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int grp = it / f.tiles, tile = it - grp * f.tiles;
+    const int e = sh.g_expert[grp], n = sh.g_count[grp], row0 = e * f.rows + tile * f.step;
+    const uint16_t* list = sh.list + sh.g_first[grp];
+    const float gs = FMT == kNv && f.m->gscale ? __ldg(f.m->gscale + e * f.m->gstride) : 1.0f;
+    // the powers of the columns that this thread will write, on their way while the products run
+    float pow[NT] = {};
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+        const int c = WHICH == 0 ? warp : tid / TILE + 8 * k;
+        if (c < n) {
+            if (WHICH == 0) {
+                if (k == 0) pow[0] = __ldcg(p.xpow + list[c] / p.top_k);
+            } else {
+                float inv;
+                power_of(__ldcg(p.hmax + list[c]), pow[k], inv);
+            }
+        }
+    }
+    float acc[2][NT][4] = {};
+    item<FMT, NT, WHICH>(p, sh.plan, ring, smem_of(sh.full), smem_of(sh.empty), f, row0, n, cur, acc);
+
+    const int g = lane >> 2, t = lane & 3, half = (warp >> 2) & 1;
+    const int slice = (warp >> 3) * 4 + (warp & 3), rho = (g >> 1) | ((g & 1) << 2);
+    if (wait_first) consumers_sync();                        // the last item's readers are done
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int c = 0; c < NT; ++c)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                buf[(slice * TILE + 32 * i + 16 * half + rho + 8 * (j >> 1)) * PITCH + 8 * c + 2 * t + (j & 1)] =
+                    acc[i][c][j];
+    consumers_sync();
+    if (WHICH == 0) {
+        // a warp per pair: 32 consecutive values of h share a power of two
+        const int c = warp;
+        if (c < n) {
+            float a = 0.0f, b = 0.0f;
+#pragma unroll
+            for (int k = 0; k < SLICES; ++k) {
+                a += buf[(k * TILE + lane) * PITCH + c];
+                b += buf[(k * TILE + 32 + lane) * PITCH + c];
+            }
+            a = __fmul_rn(__fmul_rn(a, gs), pow[0]);
+            b = __fmul_rn(__fmul_rn(b, gs), pow[0]);
+            const float v = __fmul_rn(__fdiv_rn(a, 1.0f + expf(-a)), b);
+            const uint32_t top = __reduce_max_sync(0xffffffffu, finite_bits(v));
+            float own, inv;
+            power_of(top, own, inv);
+            const int pair = list[c];
+            __half* h = p.h + (int64_t)pair * p.ip;
+            float* hpow = p.hpow + (int64_t)pair * (p.ip / 32);
+            h[place<FMT>(tile * 32 + lane)] = __float2half_rn(__fmul_rn(v, inv));
+            if (lane == 0) {
+                hpow[tile] = own;
+                atomicMax(p.hmax + pair, top);
+            }
+            if (tile == f.tiles - 1)                         // zeros to the end of the padded row
+                for (int k = tile + 1; k < p.ip / 32; ++k) {
+                    h[place<FMT>(k * 32 + lane)] = __float2half_rn(0.0f);
+                    if (lane == 0) hpow[k] = 0.0f;
+                }
+        }
+    } else {
+        const int r = tid & (TILE - 1);
+        if (tile * TILE + r < p.hidden) {
+#pragma unroll
+            for (int k = 0; k < NT; ++k) {
+                const int c = tid / TILE + 8 * k;
+                if (c < n) {
                     float a = 0.0f;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) a += buf[(k * TILE + r) * PITCH + c];
-                    p.o[(int64_t)list[c] * p.hidden + tile * TILE + r] = __fmul_rn(a, gs);
+                    for (int l = 0; l < SLICES; ++l) a += buf[(l * TILE + r) * PITCH + c];
+                    p.o[(int64_t)list[c] * p.hidden + tile * TILE + r] = __fmul_rn(__fmul_rn(a, gs), pow[k]);
                 }
+            }
         }
+    }
+}
+
+// The consumer warps' part of one phase.
+template <int FMT, int WHICH>
+__device__ void multiply(const Params& p, const Shared& sh, uint32_t ring, float* red, Cursor& cur)
+{
+    const Phase f = phase_of(p, sh.plan, WHICH);
+    bool wide_before = true;
+    int turn = 0;
+    for (int it = f.first; it < f.items; it += gridDim.x) {
+        // items of up to 8 columns alternate between two buffers and need no wait for the readers of the one before
+        const bool wide = sh.g_count[it / f.tiles] > 8;
+        if (wide) {
+            whole_item<FMT, 2, WHICH>(p, sh, ring, red, f, it, true, cur);
+        } else {
+            whole_item<FMT, 1, WHICH>(p, sh, ring, red + turn * (SLICES * TILE * 9), f, it, wide_before, cur);
+            turn ^= 1;
+        }
+        wide_before = wide;
     }
 }
 
@@ -754,7 +1013,6 @@ __device__ __forceinline__ void consumers_count(unsigned int* counter)
     consumers_sync();
     if (threadIdx.x == 0) {
         __threadfence();
-        fence_async();
         atomicAdd(counter, 1u);
     }
 }
@@ -770,26 +1028,32 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(const __grid_constant__
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < MAX_STAGES; ++i) {
-            tc::mbar_init(smem_of(&sh.full[i]), 2u);
-            tc::mbar_init(smem_of(&sh.empty[i]), (uint32_t)CONSUMERS);
+            // the weights' bytes, the lanes that copy scale bytes and activations, and a lane for each warp of these
+            tc::mbar_init(smem_of(&sh.full[i]), 1u + (FMT == kF8 ? 0u : 32u) + 33u * ACT_WARPS);
+            tc::mbar_init(smem_of(&sh.empty[i]), (uint32_t)CONSUMERS / 2u);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    convert_x(p);
+    convert_x<FMT>(p, reinterpret_cast<unsigned int*>(red));
     if (p.router) route_logits(p);
     __syncthreads();
     if (threadIdx.x == 0) {
         __threadfence();
-        fence_async();
         atomicAdd(&p.ctl->start, 1u);
         spin(&p.ctl->start, gridDim.x, p.fault);
     }
     __syncthreads();
     if (p.router) {
-        choose(p, sh);
+        if (p.experts <= 32)
+            choose<1>(p, sh);
+        else if (p.experts <= 128)
+            choose<4>(p, sh);
+        else
+            choose<MAX_EXPERTS / 32>(p, sh);
     } else {
         for (int i = threadIdx.x; i < p.tokens * p.top_k; i += THREADS) {
-            sh.id[i] = p.ids[i];
+            const int e = p.ids[i];
+            sh.id[i] = (unsigned)e < (unsigned)p.experts ? (uint16_t)e : (uint16_t)NONE;
             sh.w[i] = p.weights[i];
         }
     }
@@ -797,24 +1061,20 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(const __grid_constant__
     make_plan<FMT>(p, sh);
 
     if (warp < CONSUMERS) {
-        int s = 0;
-        uint32_t ph = 0;
-        bool live = true;
-        const bool narrow = sh.plan.widest <= 8;
-        if (narrow)
-            multiply<FMT, 1>(p, sh, ring, red, 0, s, ph, live);
-        else
-            multiply<FMT, 2>(p, sh, ring, red, 0, s, ph, live);
+        Cursor cur{0, 0u, 0u, true};
+        multiply<FMT, 0>(p, sh, ring, red, cur);
         consumers_count(&p.ctl->h_done);
-        if (narrow)
-            multiply<FMT, 1>(p, sh, ring, red, 1, s, ph, live);
-        else
-            multiply<FMT, 2>(p, sh, ring, red, 1, s, ph, live);
+        // the pairs' maxima are read directly, not through a stage
+        if ((threadIdx.x & 31) == 0) cur.live = spin(&p.ctl->h_done, gridDim.x, p.fault) && cur.live;
+        cur.live = __all_sync(0xffffffffu, cur.live);
+        multiply<FMT, 1>(p, sh, ring, red, cur);
         consumers_count(&p.ctl->o_done);
     } else if (warp == CONSUMERS) {
         stream_weights<FMT>(p, sh, ring);
+    } else if (warp == CONSUMERS + 1) {
+        if constexpr (FMT != kF8) stream_scales<FMT>(p, sh, ring);
     } else {
-        stream_activations<FMT>(p, sh, ring);
+        stream_activations<FMT>(p, sh, ring, warp - CONSUMERS - 2);
     }
     __syncthreads();
     if (threadIdx.x == 0) spin(&p.ctl->o_done, gridDim.x, p.fault);
@@ -827,7 +1087,7 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(const __grid_constant__
         float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         for (int k = 0; k < p.top_k; ++k) {
             const int pair = t * p.top_k + k;
-            if ((unsigned)sh.id[pair] >= (unsigned)p.experts) continue;
+            if (sh.id[pair] == NONE) continue;
             const float w = sh.w[pair];
             const float4 v = __ldcg(reinterpret_cast<const float4*>(p.o + (int64_t)pair * p.hidden + c));
             sum.x = __fmaf_rn(w, v.x, sum.x);
@@ -850,23 +1110,25 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(const __grid_constant__
 }
 
 // ---------------------------------------------------------------- host
+int64_t padded(int64_t v) { return (v + 127) & ~(int64_t)127; }
+
 struct Layout {
-    size_t logits, xs, xsc, h, hsc, o, total;
+    size_t logits, xs, xpow, h, hpow, hmax, o, total;
 };
 
 Layout layout(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k)
 {
-    auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
-    const size_t pairs = (size_t)(tokens * top_k);
-    const size_t hb = (size_t)((hidden / 32 + 3) & ~(int64_t)3), ib = (size_t)((inter / 32 + 3) & ~(int64_t)3);
+    auto up = [](int64_t v) { return (size_t)((v + 255) & ~(int64_t)255); };
+    const int64_t pairs = tokens * top_k;
     Layout l;
     l.logits = 256;
-    l.xs = l.logits + up((size_t)(tokens * experts) * 4);
-    l.xsc = l.xs + up((size_t)(tokens * hidden) * 2);
-    l.h = l.xsc + up((size_t)tokens * hb * 4);
-    l.hsc = l.h + up(pairs * (size_t)inter * 2);
-    l.o = l.hsc + up(pairs * ib * 4);
-    l.total = l.o + up(pairs * (size_t)hidden * 4);
+    l.xs = l.logits + up(8 * tokens * experts * 4);
+    l.xpow = l.xs + up(tokens * padded(hidden) * 2);
+    l.h = l.xpow + up(tokens * 4);
+    l.hpow = l.h + up(pairs * padded(inter) * 2);
+    l.hmax = l.hpow + up(pairs * padded(inter) / 32 * 4);
+    l.o = l.hmax + up(pairs * 4);
+    l.total = l.o + up(pairs * hidden * 4);
     return l;
 }
 
@@ -954,9 +1216,10 @@ extern "C" int fp4q_moe(const void* x, int64_t tokens, int64_t hidden, int64_t i
     p.ctl = reinterpret_cast<Control*>(ws);
     p.logits = reinterpret_cast<float*>(ws + l.logits);
     p.xs = reinterpret_cast<__half*>(ws + l.xs);
-    p.xsc = reinterpret_cast<float*>(ws + l.xsc);
+    p.xpow = reinterpret_cast<float*>(ws + l.xpow);
     p.h = reinterpret_cast<__half*>(ws + l.h);
-    p.hsc = reinterpret_cast<float*>(ws + l.hsc);
+    p.hpow = reinterpret_cast<float*>(ws + l.hpow);
+    p.hmax = reinterpret_cast<unsigned int*>(ws + l.hmax);
     p.o = reinterpret_cast<float*>(ws + l.o);
     p.tokens = (int)tokens;
     p.hidden = (int)hidden;
@@ -964,8 +1227,8 @@ extern "C" int fp4q_moe(const void* x, int64_t tokens, int64_t hidden, int64_t i
     p.experts = (int)experts;
     p.top_k = (int)top_k;
     p.normalize = normalize != 0;
-    p.hb = (int)((hidden / 32 + 3) & ~(int64_t)3);
-    p.ib = (int)((inter / 32 + 3) & ~(int64_t)3);
+    p.hp = (int)padded(hidden);
+    p.ip = (int)padded(inter);
     p.fault = device_fault_word();
     if (!p.fault) return FP4Q_ERR_CUDA;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);

@@ -7,15 +7,17 @@ Bars (u = 2^-24, s(.) sums of magnitudes):
   top_k up to 2 d, in descending order up to 2 d; equal router rows give equal
   logits and the lower expert.  A weight exp(l_j - l_max) / sum differs by a
   factor of 1 + 4 d (two logits above, two below) and 2^-20 for expf and the sum.
-- gate and up: E = (hidden / 128 + 24) u s(W x) + 2^-25 s(W max32|x|): each of
-  the four quarters adds a block of 32 with one rounding, a block's own products
-  and scales take at most 16 more, four quarters 4, slack 4; x as fp16 is exact
-  to 2^-25 of the largest of its 32 values.
+- gate and up: E = (hidden / 64 + 24) u s(W x) + 2^-32 s(W) max|x|: each of the
+  eight slices of k adds 16 products with one rounding, or truncation (2 u); a
+  product's own alignment, scales and the slices take at most 24 more; x as fp16
+  under its row's power of two is off by at most half of 2^-24 where the row's
+  largest value is at least 2^7.
 - h = silu(g) u has |silu'| <= 1.1 and is held as fp16: 11 significant bits, so
   its values lie 2^-10 of their power of two apart and rounding moves one by at
-  most half of that, 2^-11 of itself (and 2^-25 of the largest of its 32): Eh =
-  1.1 Eg (|u| + Eu) + |silu(g)| Eu + (2^-11 + 2^-20) |h| + 2^-25 max32|h|.
-- y: s(w D Eh) + (inter / 128 + 24 + top_k) u s(w D h) + half an ulp of bf16,
+  most half of that, 2^-11 of itself; brought to the row's power a value may
+  lose all below 2^-24 of the row's largest: Eh = 1.1 Eg (|u| + Eu) +
+  |silu(g)| Eu + (2^-11 + 2^-20) |h| + 2^-24 max|h|.
+- y: s(w D Eh) + (inter / 64 + 24 + top_k) u s(w D h) + half an ulp of bf16,
   with the weights the call returned.
 """
 import pytest
@@ -68,8 +70,8 @@ def decode(w, fmt, experts):
     return v if g is None else v * g.cpu().double().view(-1, 1, 1)
 
 
-def max32(v):
-    return v.abs().view(v.shape[0], -1, 32).amax(2).repeat_interleave(32, 1)
+def top_of(v):
+    return v.abs().amax(1, keepdim=True)
 
 
 def layer64(x, up, down, ids, weights):
@@ -84,13 +86,13 @@ def layer64(x, up, down, ids, weights):
             continue
         xe, W, D, we = x[token], up[e], down[e], w[token, slot][:, None]
         v = xe @ W.T
-        ev = (hidden / 128 + 24) * U * (xe.abs() @ W.abs().T) + 2.0 ** -25 * (max32(xe) @ W.abs().T)
+        ev = (hidden / 64 + 24) * U * (xe.abs() @ W.abs().T) + 2.0 ** -32 * top_of(xe) * W.abs().sum(1)
         g, u, eg, eu = v[:, :inter], v[:, inter:], ev[:, :inter], ev[:, inter:]
         silu = g * torch.sigmoid(g)
         h = silu * u
-        eh = 1.1 * eg * (u.abs() + eu) + silu.abs() * eu + (2.0 ** -11 + 2.0 ** -20) * h.abs() + 2.0 ** -25 * max32(h)
+        eh = 1.1 * eg * (u.abs() + eu) + silu.abs() * eu + (2.0 ** -11 + 2.0 ** -20) * h.abs() + 2.0 ** -24 * top_of(h)
         y.index_add_(0, token, (h @ D.T) * we)
-        far.index_add_(0, token, (eh @ D.abs().T + (inter / 128 + 24 + top_k) * U * ((h.abs() + eh) @ D.abs().T))
+        far.index_add_(0, token, (eh @ D.abs().T + (inter / 64 + 24 + top_k) * U * ((h.abs() + eh) @ D.abs().T))
                        * we.abs())
     half = torch.finfo(torch.bfloat16).eps / 2
     return y, far * (1 + half) + half * y.abs()
