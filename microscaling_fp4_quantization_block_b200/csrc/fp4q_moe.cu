@@ -10,16 +10,17 @@
 // being up to 16 pairs of one expert, first of the gate/up matrices (32 rows
 // of each), then of the down matrices.  Per CTA
 //   warp 16 streams the items' weight rows through a ring of shared-memory
-//     stages (TMA tiles of 32 rows x 128 bytes, 128-byte swizzle), warp 17 the
-//     rows' scale bytes (16-byte cp.async: as bulk copies of 32 bytes they took
-//     45 ns each, one after the other, eight times the weights' time).  They run ahead of the layer's dependencies:
-//     the first down tiles are on their way while h is still being computed;
-//   warps 18 and 19 add the pairs' activations to the stages, the down items'
-//     once all of h is written;
+//     stages (TMA tiles of 32 rows x 128 bytes, 128-byte swizzle).  It runs ahead
+//     of the layer's dependencies: the first down tiles are on their way while h
+//     is still being computed;
+//   warps 17 and 18 take turns to add the rows' scale bytes and the pairs'
+//     activations (16-byte cp.async: as bulk copies of 32 bytes the scale bytes
+//     took 45 ns each, one after the other, eight times the weights' time);
 //   warps 0-15 multiply: two sets take turns at the stages, in a set 4 quarters
 //     of the stage's k by 2 halves of its rows, mma.sync m16n8k16 with the
-//     weights as the 16 rows and the pairs as the 8 columns; an item ends with
-//     the sum of the eight slices of k.
+//     weights as the 16 rows and the pairs as the 8 columns;
+//   warps 20-23 add the eight slices of k and finish the item (silu, h; or the
+//     pairs' results) while the next one is multiplied.
 // The weights are widened to fp16 in registers on their way from shared memory
 // into the product; tcgen05.mma, whose operands lie in shared or tensor
 // memory, would need them written back first, and with a few columns per
@@ -34,8 +35,8 @@
 // UE4M3 scale; E8M0 and fp32 scales multiply the fp32 sums of their blocks.
 //
 // Sums across k are in a fixed order and a token's pairs are added in slot
-// order, so results do not depend on timing.  The three points where all CTAs
-// wait for one another (x and logits ready, h ready, pair results ready) count
+// order, so results do not depend on timing.  The points where all CTAs
+// wait for one another (x and logits, choices, h, pair results) count
 // in the workspace; the launch is cooperative, so all CTAs are resident, and
 // every wait is bounded: one that runs out records the library's fault word
 // and its warp goes on without waiting, within bounds, to the end.
@@ -57,16 +58,21 @@ namespace moe {
 constexpr int MAX_TOKENS = FP4Q_MOE_MAX_TOKENS, MAX_TOPK = FP4Q_MOE_MAX_TOPK, MAX_EXPERTS = FP4Q_MOE_MAX_EXPERTS;
 constexpr int MAX_PAIRS = MAX_TOKENS * MAX_TOPK;
 constexpr int CONSUMERS = 16;                           // warps that multiply, two sets of 8
-constexpr int ACT_WARPS = 2;
-constexpr int THREADS = 32 * (CONSUMERS + 2 + ACT_WARPS);
+constexpr int AUX_WARPS = 2;                            // that copy scale bytes and activations
+constexpr int SPARE_WARPS = 1;                          // so that each warpgroup has registers of its own
+constexpr int SUM_WARPS = 4;                            // that add an item's slices and write its results
+constexpr int THREADS = 32 * (CONSUMERS + 1 + AUX_WARPS + SPARE_WARPS + SUM_WARPS);
+constexpr int REGS_PRODUCTS = 88, REGS_OTHERS = 64;     // 512 x 88 + 256 x 64 = 768 x 80, the launch's registers
 constexpr int GROUP = 16;                               // pairs per group, at most
 constexpr int TILE = 64;                                // rows per item: two boxes of 32
 constexpr int BOX_BYTES = 32 * 128;
+constexpr int WEIGHT_BYTES = 2 * 2 * BOX_BYTES;         // per stage: two 128-byte chunks of two boxes
 constexpr int SLICES = CONSUMERS / 2;                   // of k, per item
 constexpr int RING_BYTES = 172 * 1024;
-constexpr int RED_BYTES = 36 * 1024;                    // two buffers of 8 columns or one of 16
+constexpr int RED_BYTES = 36 * 1024;                    // partial sums: two buffers of 8 columns or one of 16
 constexpr int SMEM_BYTES = 1024 + RING_BYTES + RED_BYTES;
 constexpr int MAX_STAGES = 12;
+constexpr int MIN_STAGES = 4;
 constexpr uint32_t NONE = 0xffffu;
 constexpr uint32_t kMaxSpins = 1u << 22;                // polls of a counter in global memory (about 1 us each)
 
@@ -93,35 +99,37 @@ struct Params {
     uint16_t* y;                    // bf16 [tokens][hidden]
     Control* ctl;
     float* logits;                  // [slices of k][tokens][experts]
-    __half* xs;                     // [tokens][hp]: rows padded with zeros to hp values
+    uint8_t* xs;                    // [tokens][xstages] records (Format::RECORD bytes)
     float* xpow;                    // [tokens]
-    __half* h;                      // [pairs][ip]
-    float* hpow;                    // [pairs][ip / 32]
+    uint8_t* h;                     // [pairs][hstages] records
     unsigned int* hmax;             // [pairs]: pattern of the largest finite |h|
     float* o;                       // [pairs][hidden]
     int tokens, hidden, inter, experts, top_k, normalize;
-    int hp, ip;                     // hidden and inter, rounded up to 128
+    int xstages, hstages;           // stages of hidden and of inter values
     unsigned int* fault;
 };
 
 struct Plan {                       // what the CTA knows once the choices are made
     int groups;                     // (expert, up to GROUP pairs)
     int widest;                     // pairs of the largest group
-    int stages;                     // an even number: a slot of the ring belongs to one set of warps
-    uint32_t aux_bytes, acts_at, pows_at;       // what a stage holds beside its weights: scale bytes, activations, powers
+    int pitch, buffers;             // of the partial sums: floats per row, and how many
+    int stages;                     // an even number: a slot of the ring belongs to one set of product warps and one aux warp
+    uint32_t aux_bytes, acts_at, inverse_at;    // what a stage holds beside its weights: scale bytes, records, 1 / the rows' powers
 };
 
 struct Shared {
     uint16_t id[MAX_PAIRS];                     // NONE: no expert
-    uint16_t place[MAX_PAIRS];                  // among the pairs of its expert
+    int count[MAX_EXPERTS];                     // pairs by expert
     float w[MAX_PAIRS];
     uint16_t list[MAX_PAIRS];                   // pairs by expert, then by number
     uint16_t first[MAX_EXPERTS + 1];            // an expert's pairs in the list
     uint16_t g_expert[MAX_PAIRS], g_first[MAX_PAIRS];
     uint8_t g_count[MAX_PAIRS];
     uint64_t full[MAX_STAGES], empty[MAX_STAGES];
+    uint64_t summed[2], summable[2];            // a buffer of partial sums: free, complete
     Plan plan;
 };
+static_assert(AUX_WARPS == 2 && MIN_STAGES > AUX_WARPS, "the ring is even");
 static_assert(sizeof(Shared) + SMEM_BYTES + 1024 <= 227 * 1024, "shared memory per CTA");
 
 // ---------------------------------------------------------------- formats
@@ -134,12 +142,14 @@ struct Format {
     static constexpr int BLOCKS = VALUES / 32;
     static constexpr int SCALE_BYTES = FMT == kNv ? VALUES / 16 : FMT == kMx ? VALUES / 32 : 0;   // per row and stage
     static constexpr int SCALE_PITCH = SCALE_BYTES ? SCALE_BYTES + 16 : 0;
-    static constexpr int ACT_PITCH = VALUES * 2 + 64;        // 64 mod 128: 16-byte reads by (pair, lane) hit all banks
-    static constexpr int POW_PITCH = BLOCKS + 4;             // floats: the blocks' powers, then the row's inverse
+    // A row's activations of one stage, as they are kept and copied: fp16 values (zeros past the row's end), then
+    // the powers of two of its blocks of 32 (h only).  64 mod 128 bytes: 16-byte reads by (pair, lane) hit all banks.
+    static constexpr int POWERS = VALUES * 2, RECORD = POWERS + 64;
+    static constexpr int AUX_MOST = TILE * SCALE_PITCH + GROUP * (RECORD + 4);
+    static_assert(MIN_STAGES * (WEIGHT_BYTES + AUX_MOST) <= RING_BYTES, "a ring of at least four stages");
 };
-constexpr int WEIGHT_BYTES = 2 * 2 * BOX_BYTES;              // per stage: two chunks of two boxes
 
-// Where value i of a row of activations is kept.  In the products a lane t of
+// Where value i of a stage's activations is kept.  In the products a lane t of
 // four holds 16 bytes of a row's 64-byte quarter: 32 E2M1 values (one block, or
 // under E8M0 scales a quarter of each of four blocks) or 16 E4M3 values.  The
 // activations are stored so that the lane's 16-byte pieces j of one quarter lie
@@ -161,11 +171,8 @@ __device__ __forceinline__ uint32_t ld_acquire(const unsigned int* p)
     return v;
 }
 
-// Arrive on the mbarrier when this thread's cp.async copies so far have landed.
-__device__ __forceinline__ void arrive_on_copies(uint32_t bar)
-{
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
-}
+// What other threads stored, for this thread's bulk copies.
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 // Wait until `n` CTAs have counted; false (and the fault word set) when the wait runs out.
 __device__ bool spin(const unsigned int* counter, unsigned int n, unsigned int* fault)
@@ -205,6 +212,7 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi)
 template <int FMT>
 __device__ void convert_x(const Params& p, unsigned int* part)
 {
+    using F = Format<FMT>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int i = blockIdx.x * THREADS + threadIdx.x; i < p.tokens * p.top_k; i += gridDim.x * THREADS) p.hmax[i] = 0u;
     for (int t = blockIdx.x; t < p.tokens; t += gridDim.x) {
@@ -224,14 +232,16 @@ __device__ void convert_x(const Params& p, unsigned int* part)
         float pow, inv;
         power_of(m, pow, inv);
         if (threadIdx.x == 0) p.xpow[t] = pow;
-        for (int c = threadIdx.x * 8; c < p.hp; c += THREADS * 8) {
+        uint8_t* to = p.xs + (int64_t)t * p.xstages * F::RECORD;
+        for (int c = threadIdx.x * 8; c < p.xstages * F::VALUES; c += THREADS * 8) {
             uint4 w = make_uint4(0u, 0u, 0u, 0u);
             if (c < p.hidden) w = *reinterpret_cast<const uint4*>(x + c);
             const uint32_t v[4] = {w.x, w.y, w.z, w.w};
             uint32_t r[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) r[j] = f16x2(__fmul_rn(bf16_lo(v[j]), inv), __fmul_rn(bf16_hi(v[j]), inv));
-            *reinterpret_cast<uint4*>(p.xs + (int64_t)t * p.hp + place<FMT>(c)) = make_uint4(r[0], r[1], r[2], r[3]);
+            *reinterpret_cast<uint4*>(to + c / F::VALUES * F::RECORD + 2 * place<FMT>(c % F::VALUES)) =
+                make_uint4(r[0], r[1], r[2], r[3]);
         }
         __syncthreads();                                     // part is free again
     }
@@ -311,10 +321,10 @@ __device__ __forceinline__ float from_ordered(uint32_t k)
 
 // The top_k experts of every token and their weights, a warp per token; a lane holds PER experts.
 template <int PER>
-__device__ void choose(const Params& p, Shared& sh)
+__device__ void choose(const Params& p, Shared& sh, int first, int step, bool tell)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slices = logit_slices(p);
-    for (int t = warp; t < p.tokens; t += THREADS / 32) {
+    const int lane = threadIdx.x & 31, slices = logit_slices(p);
+    for (int t = first; t < p.tokens; t += step) {
         uint32_t key[PER];
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
@@ -368,7 +378,7 @@ __device__ void choose(const Params& p, Shared& sh)
             const float w = __fdiv_rn(mine, below);
             sh.id[t * p.top_k + lane] = (uint16_t)chosen;
             sh.w[t * p.top_k + lane] = w;
-            if (blockIdx.x == 0) {
+            if (tell) {
                 p.ids[t * p.top_k + lane] = (int)chosen;
                 p.weights[t * p.top_k + lane] = w;
             }
@@ -382,25 +392,16 @@ __device__ void make_plan(const Params& p, Shared& sh)
 {
     using F = Format<FMT>;
     const int pairs = p.tokens * p.top_k, lane = threadIdx.x & 31;
-    for (int e = threadIdx.x; e <= p.experts; e += THREADS) sh.first[e] = 0;
+    for (int e = threadIdx.x; e < p.experts; e += THREADS) sh.count[e] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < pairs; i += THREADS)
+        if (sh.id[i] != NONE) atomicAdd(&sh.count[sh.id[i]], 1);
     __syncthreads();
     if (threadIdx.x < 32) {
-        // a pair's place among its expert's, 32 pairs at a time; the counts build up in first[e + 1]
-        for (int i = lane; i < ((pairs + 31) & ~31); i += 32) {
-            const uint32_t e = i < pairs ? sh.id[i] : NONE;
-            const uint32_t same = __match_any_sync(0xffffffffu, e);
-            const int ahead = __popc(same & ((1u << lane) - 1u)), n = e != NONE ? sh.first[e + 1] : 0;
-            __syncwarp();
-            if (e != NONE) {
-                sh.place[i] = (uint16_t)(n + ahead);
-                if (ahead == 0) sh.first[e + 1] = (uint16_t)(n + __popc(same));
-            }
-            __syncwarp();
-        }
         int total = 0, groups = 0, widest = 0;
         for (int e0 = 0; e0 < p.experts; e0 += 32) {
             const int e = e0 + lane;
-            const int n = e < p.experts ? sh.first[e + 1] : 0;
+            const int n = e < p.experts ? sh.count[e] : 0;
             const int ng = (n + GROUP - 1) / GROUP;
             int sn = n, sg = ng;
 #pragma unroll
@@ -416,27 +417,44 @@ __device__ void make_plan(const Params& p, Shared& sh)
                 sh.g_count[g] = (uint8_t)c;
             }
             widest = max(widest, min(GROUP, n));
-            __syncwarp();
             if (e < p.experts) sh.first[e] = (uint16_t)at;
             total += __shfl_sync(0xffffffffu, sn, 31);
             groups += __shfl_sync(0xffffffffu, sg, 31);
-            // the next 32 counts start at first[e0 + 33]; first[e0 + 32] is overwritten by them only
-            __syncwarp();
         }
+        if (lane == 0) sh.first[p.experts] = (uint16_t)total;
         widest = __reduce_max_sync(0xffffffffu, widest);
         if (lane == 0) {
             Plan& q = sh.plan;
             q.groups = groups;
             q.widest = widest;
+            q.pitch = widest > 8 ? 17 : 9;
+            q.buffers = widest > 8 ? 1 : 2;
             q.acts_at = TILE * F::SCALE_PITCH;
-            q.pows_at = q.acts_at + widest * F::ACT_PITCH;
-            q.aux_bytes = q.pows_at + widest * F::POW_PITCH * 4;
+            q.inverse_at = q.acts_at + widest * F::RECORD;
+            q.aux_bytes = (q.inverse_at + widest * 4 + 15u) & ~15u;
             q.stages = min(MAX_STAGES, (int)(RING_BYTES / (WEIGHT_BYTES + q.aux_bytes))) & ~1;
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < pairs; i += THREADS)
-        if (sh.id[i] != NONE) sh.list[sh.first[sh.id[i]] + sh.place[i]] = (uint16_t)i;
+    // Within a group the order of the pairs changes nothing; which group a pair
+    // of a long list falls into must be the same in every CTA: by number.
+    for (int i = threadIdx.x; i < pairs; i += THREADS) {
+        const uint32_t e = sh.id[i];
+        if (e != NONE && sh.first[e + 1] - sh.first[e] <= GROUP)
+            sh.list[sh.first[e] + atomicSub(&sh.count[e], 1) - 1] = (uint16_t)i;
+    }
+    if (sh.plan.widest == GROUP) {
+        for (int e = threadIdx.x >> 5; e < p.experts; e += THREADS / 32) {
+            int at = sh.first[e];
+            if (sh.first[e + 1] - at <= GROUP) continue;
+            for (int i = lane; i < ((pairs + 31) & ~31); i += 32) {
+                const bool mine = i < pairs && sh.id[i] == (uint32_t)e;
+                const uint32_t all = __ballot_sync(0xffffffffu, mine);
+                if (mine) sh.list[at + __popc(all & ((1u << lane) - 1u))] = (uint16_t)i;
+                at += __popc(all);
+            }
+        }
+    }
     __syncthreads();
 }
 
@@ -479,29 +497,34 @@ __device__ __forceinline__ Phase phase_of(const Params& p, const Plan& q, int wh
     return f;
 }
 
-// The places of this CTA's stages, in order.
+// A place in the CTA's sequence of stages, `step` stages at a time.  step divides
+// the ring, so that a slot always belongs to the same warp: a barrier's parity
+// tells a phase only from the one before it, so whoever waits for a slot must
+// have seen each of its rounds.
 struct Slots {
     uint32_t full0, empty0;
-    int n, at;
+    int n, step, at;
     uint32_t phase;
 
-    __device__ Slots(const Shared& sh)
-        : full0(smem_of(sh.full)), empty0(smem_of(sh.empty)), n(sh.plan.stages), at(0), phase(1u) {}
+    __device__ Slots(const Shared& sh, int first, int by)
+        : full0(smem_of(sh.full)), empty0(smem_of(sh.empty)), n(sh.plan.stages), step(by), at(first), phase(1u) {}
     __device__ __forceinline__ bool wait_empty(unsigned int* fault) const
     {
-        return __all_sync(0xffffffffu, tc::wait_phase(empty0 + 8u * at, phase, fault));
+        return tc::wait_phase(empty0 + 8u * at, phase, fault);
     }
     __device__ __forceinline__ void next()
     {
-        if (++at == n) at = 0, phase ^= 1u;
+        at += step;
+        if (at >= n) at -= n, phase ^= 1u;                   // step is below n
     }
 };
 
+// One lane.
 template <int FMT>
-__device__ void stream_weights(const Params& p, const Shared& sh, uint32_t ring)
+__device__ __forceinline__ void stream_weights(const Params& p, const Shared& sh, uint32_t ring)
 {
     using F = Format<FMT>;
-    Slots s(sh);
+    Slots s(sh, 0, 1);
     for (int which = 0; which < 2; ++which) {
         const Phase f = phase_of(p, sh.plan, which);
         const int row_bytes = F::f8 ? f.k : f.k / 2;
@@ -510,134 +533,96 @@ __device__ void stream_weights(const Params& p, const Shared& sh, uint32_t ring)
             const int row0 = sh.g_expert[g] * f.rows + tile * f.step;      // experts * rows is below 2^31
             for (int b0 = 0; b0 < row_bytes; b0 += F::CHUNKS * 128) {
                 if (!s.wait_empty(p.fault)) return;
-                if ((threadIdx.x & 31) == 0) {
-                    const uint32_t st = ring + (uint32_t)(s.at * WEIGHT_BYTES), bar = s.full0 + 8u * s.at;
-                    const int chunks = min(F::CHUNKS, (row_bytes - b0 + 127) / 128);
-                    tc::mbar_expect_tx(bar, (uint32_t)(chunks * 2 * BOX_BYTES));
-                    for (int c = 0; c < chunks; ++c) {
-                        tc::tma_load_2d(st + (uint32_t)(c * 2 * BOX_BYTES), &f.m->map, b0 + c * 128, row0, bar);
-                        tc::tma_load_2d(st + (uint32_t)(c * 2 * BOX_BYTES + BOX_BYTES), &f.m->map, b0 + c * 128,
-                                        row0 + f.second, bar);
-                    }
+                const uint32_t st = ring + (uint32_t)(s.at * WEIGHT_BYTES), bar = s.full0 + 8u * s.at;
+                const bool two = b0 + 128 < row_bytes;
+                tc::mbar_expect_tx(bar, two ? 4u * BOX_BYTES : 2u * BOX_BYTES);
+                tc::tma_load_2d(st, &f.m->map, b0, row0, bar);
+                tc::tma_load_2d(st + BOX_BYTES, &f.m->map, b0, row0 + f.second, bar);
+                if (two) {
+                    tc::tma_load_2d(st + 2 * BOX_BYTES, &f.m->map, b0 + 128, row0, bar);
+                    tc::tma_load_2d(st + 3 * BOX_BYTES, &f.m->map, b0 + 128, row0 + f.second, bar);
                 }
-                __syncwarp();
                 s.next();
             }
         }
     }
 }
 
-// The rows' scale bytes, widened to 16-byte boundaries (every matrix of scales
-// ends on one): a lane's rows and its pieces of them are the same all through
-// an item.
+// What a stage holds beside its weights: the rows' scale bytes, widened to
+// 16-byte boundaries (every matrix of scales ends on one), and the pairs'
+// activations.  AUX_WARPS warps take turns at the stages: one warp alone took
+// 0.35 us a stage, as long as HBM needs for its weights.
 template <int FMT>
-__device__ void stream_scales(const Params& p, const Shared& sh, uint32_t ring)
+__device__ __forceinline__ void stream_aux(const Params& p, const Shared& sh, uint32_t ring, int turn)
 {
     using F = Format<FMT>;
-    constexpr int PIECES = F::SCALE_PITCH / 16, MINE = TILE * PIECES / 32;
+    constexpr int PIECES = F::SCALE_PITCH / 16, MINE = TILE * PIECES / 32;  // of 16 bytes: per row, per lane
     const int lane = threadIdx.x & 31;
-    Slots s(sh);
-    uint32_t dst[MINE];
-#pragma unroll
-    for (int i = 0; i < MINE; ++i) {
-        const int r = (lane + 32 * i) / PIECES;
-        dst[i] = (uint32_t)(r * F::SCALE_PITCH + 16 * ((lane + 32 * i) - r * PIECES));
-    }
+    const uint32_t aux0 = ring + (uint32_t)sh.plan.stages * WEIGHT_BYTES, aux_bytes = sh.plan.aux_bytes;
+    const uint32_t act_at = sh.plan.acts_at + (uint32_t)(lane * F::RECORD), inverse_at = sh.plan.inverse_at + 4u * lane;
+    Slots s(sh, turn, AUX_WARPS);
+    int ahead = turn;                                        // stages before this warp's next one
+    fence_async();                                           // x was converted by ordinary stores
     for (int which = 0; which < 2; ++which) {
         const Phase f = phase_of(p, sh.plan, which);
-        const int srb = f.k / (FMT == kNv ? 16 : 32);
-        const uint8_t* scales = static_cast<const uint8_t*>(f.m->scales);
+        const int srb = f.k / (FMT == kNv ? 16 : 32), stages = which == 0 ? p.xstages : p.hstages;
+        bool ready = which == 0;
         for (int it = f.first; it < f.items; it += gridDim.x) {
-            const int g = it / f.tiles, tile = it - g * f.tiles;
+            const int g = it / f.tiles, tile = it - g * f.tiles, n = sh.g_count[g];
             const int row0 = sh.g_expert[g] * f.rows + tile * f.step;
-            const uint8_t* src[MINE];
-            int skip[MINE];                                  // row bytes that lie before the piece, less those asked for
-#pragma unroll
-            for (int i = 0; i < MINE; ++i) {
-                const int r = (lane + 32 * i) / PIECES, piece = (lane + 32 * i) - r * PIECES;
-                const int row = (r >> 5) * f.second + (r & 31);
-                const int64_t at = (int64_t)(row0 + row) * srb;
-                src[i] = scales + (at & ~(int64_t)15) + 16 * piece;
-                skip[i] = 16 * piece - (int)(at & 15);
-                if (tile * f.step + row >= f.rows) skip[i] = 1 << 30;      // the second box may lie past the expert
-            }
-            for (int from = 0; from < srb; from += F::SCALE_BYTES) {
-                if (!s.wait_empty(p.fault)) return;
-                const uint32_t aux = ring + (uint32_t)s.n * WEIGHT_BYTES + (uint32_t)s.at * sh.plan.aux_bytes;
-                const int want = min(F::SCALE_BYTES, srb - from);
+            const uint8_t* src[MINE + 1];
+            int skip[MINE + 1];                              // row bytes that lie before the piece, less those asked for
+            if constexpr (FMT != kF8) {
 #pragma unroll
                 for (int i = 0; i < MINE; ++i) {
-                    if (skip[i] < want) cp_async16(aux + dst[i], src[i], 16u);
-                    src[i] += F::SCALE_BYTES;
+                    const int r = (lane + 32 * i) / PIECES, piece = (lane + 32 * i) - r * PIECES;
+                    const int row = (r >> 5) * f.second + (r & 31);
+                    const int64_t at = (int64_t)(row0 + row) * srb;
+                    src[i] = static_cast<const uint8_t*>(f.m->scales) + (at & ~(int64_t)15) + 16 * piece;
+                    skip[i] = 16 * piece - (int)(at & 15);
+                    if (tile * f.step + row >= f.rows) skip[i] = 1 << 30;  // the second box may lie past the expert
                 }
-                arrive_on_copies(s.full0 + 8u * s.at);
-                s.next();
             }
-        }
-    }
-}
-
-// The pairs' activations: pairs `mine`, mine + ACT_WARPS, ... of each group.
-template <int FMT>
-__device__ void stream_activations(const Params& p, const Shared& sh, uint32_t ring, int mine)
-{
-    using F = Format<FMT>;
-    constexpr int MOST = GROUP / ACT_WARPS, PIECES = F::VALUES / 8;        // 16-byte pieces of a pair per stage
-    const int lane = threadIdx.x & 31;
-    const Plan& q = sh.plan;
-    Slots s(sh);
-    for (int which = 0; which < 2; ++which) {
-        const Phase f = phase_of(p, q, which);
-        if (which == 1 && f.first < f.items) {
-            const bool ok = spin(&p.ctl->h_done, gridDim.x, p.fault);
-            if (!__all_sync(0xffffffffu, ok)) return;
-        }
-        const __half* acts = which == 0 ? p.xs : p.h;
-        const int pitch = which == 0 ? p.hp : p.ip;
-        for (int it = f.first; it < f.items; it += gridDim.x) {
-            const int g = it / f.tiles, n = sh.g_count[g];
-            const uint16_t* list = sh.list + sh.g_first[g];
-            const __half* src[MOST];
-#pragma unroll
-            for (int j = 0; j < MOST; ++j) {
-                const int c = ACT_WARPS * j + mine;
-                const int row = c < n ? (which == 0 ? list[c] / p.top_k : list[c]) : 0;
-                src[j] = acts + (int64_t)row * pitch + 8 * lane;
+            int row = 0;                                     // lane c: of pair c
+            if (lane < n) {
+                row = sh.list[sh.g_first[g] + lane];
+                if (which == 0) row /= p.top_k;
             }
-            // powers of two: four lanes a pair (down items)
-            const int pc = ACT_WARPS * (lane >> 2) + mine;
-            const float* psrc = nullptr;
+            const uint8_t* acts = (which == 0 ? p.xs : p.h) + (int64_t)row * stages * F::RECORD;
             float pow, inv = 0.0f;
-            if (which == 1 && (lane >> 2) < MOST && pc < n) {
-                psrc = p.hpow + (int64_t)list[pc] * (pitch / 32) + 4 * (lane & 3);
-                power_of(__ldcg(p.hmax + list[pc]), pow, inv);
-            }
-            for (int k0 = 0; k0 < f.k; k0 += F::VALUES) {
-                if (!s.wait_empty(p.fault)) return;
-                const uint32_t aux = ring + (uint32_t)q.stages * WEIGHT_BYTES + (uint32_t)s.at * q.aux_bytes;
-                const uint32_t bar = s.full0 + 8u * s.at, to = aux + q.acts_at + (uint32_t)(mine * F::ACT_PITCH + 16 * lane);
-                const int values = min(F::VALUES, pitch - k0);
+            if (ready && which == 1 && lane < n) power_of(__ldcg(p.hmax + row), pow, inv);
+            int i = ahead;
+            for (; i < stages; i += AUX_WARPS) {
+                const bool ok = s.wait_empty(p.fault);
+                if (!__all_sync(0xffffffffu, ok)) return;
+                const uint32_t aux = aux0 + (uint32_t)s.at * aux_bytes, bar = s.full0 + 8u * s.at;
+                if constexpr (FMT != kF8) {
+                    const int from = i * F::SCALE_BYTES, want = min(F::SCALE_BYTES, srb - from);
 #pragma unroll
-                for (int j = 0; j < MOST; ++j) {
-                    if (ACT_WARPS * j + mine < n) {
-#pragma unroll
-                        for (int i = 0; i < PIECES; i += 32)
-                            if (8 * (lane + i) < values)
-                                cp_async16(to + (uint32_t)(ACT_WARPS * j * F::ACT_PITCH + 16 * i), src[j] + 8 * i, 16u);
+                    for (int j = 0; j < MINE; ++j) {
+                        const int r = (lane + 32 * j) / PIECES, piece = (lane + 32 * j) - r * PIECES;
+                        if (skip[j] < want) cp_async16(aux + (uint32_t)(r * F::SCALE_PITCH + 16 * piece), src[j] + from, 16u);
                     }
-                    src[j] += F::VALUES;
                 }
-                if (psrc) {
-                    const uint32_t pat = aux + q.pows_at + (uint32_t)(pc * F::POW_PITCH * 4);
-                    if (128 * (lane & 3) < values) cp_async16(pat + 16u * (lane & 3), psrc + k0 / 32, 16u);
-                    if ((lane & 3) == 0)
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(pat + F::BLOCKS * 4), "f"(inv) : "memory");
+                if (!ready) {                                // down items: once all of h is written
+                    const bool all = lane != 0 || spin(&p.ctl->h_done, gridDim.x, p.fault);
+                    if (!__all_sync(0xffffffffu, all)) return;
+                    fence_async();
+                    if (lane < n) power_of(__ldcg(p.hmax + row), pow, inv);
+                    ready = true;
                 }
-                arrive_on_copies(bar);
+                if (which == 1 && lane < n)
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(aux + inverse_at), "f"(inv) : "memory");
+                // one arrival per lane, when its copies have landed; one for the inverses and the records' bytes
+                if constexpr (FMT != kF8)
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(bar);         // the inverses
+                if (lane == 0) tc::mbar_expect_tx(bar, (uint32_t)(n * F::RECORD));
+                __syncwarp();
+                if (lane < n) tc::bulk_load(aux + act_at, acts + i * F::RECORD, (uint32_t)F::RECORD, bar);
                 s.next();
             }
+            ahead = i - stages;
         }
     }
 }
@@ -706,11 +691,12 @@ __device__ __forceinline__ uint32_t lds16(uint32_t a)
     return r;
 }
 
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * CONSUMERS) : "memory"); }
+__device__ __forceinline__ void sums_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * SUM_WARPS) : "memory"); }
 
 // A place in the CTA's sequence of stages.
 struct Cursor {
-    int slot;
+    uint32_t full0, empty0;
+    int stages, slot;
     uint32_t phase, seq;
     bool live;
 };
@@ -721,10 +707,11 @@ struct Cursor {
 // 128 bytes, and a 16-byte read by all lanes hits every bank.  The order of k
 // inside a product is free as long as both operands share it (see place).
 template <int FMT, int NT, int WHICH>
-__device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ring, uint32_t full0, uint32_t empty0,
-                                     const Phase& f, int row0, int n, Cursor& cur, float (&acc)[2][NT][4])
+__device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ring, const Phase& f, int row0, int n,
+                                     Cursor& cur, float (&acc)[2][NT][4])
 {
     using F = Format<FMT>;
+    const uint32_t full0 = cur.full0, empty0 = cur.empty0, aux0 = ring + (uint32_t)cur.stages * WEIGHT_BYTES;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3, half = (warp >> 2) & 1;
     const uint32_t set = (uint32_t)warp >> 3;
@@ -743,7 +730,7 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
     for (int k0 = 0; k0 < f.k; k0 += F::VALUES) {
         const int s = cur.slot;
         const uint32_t ph = cur.phase;
-        if (++cur.slot == q.stages) cur.slot = 0, cur.phase ^= 1u;
+        if (++cur.slot == cur.stages) cur.slot = 0, cur.phase ^= 1u;
         const uint32_t seq = cur.seq++;
         if ((seq & 1u) != set) continue;
         const int qi = (int)(((uint32_t)warp + (seq >> 1)) & 3u);      // turns, so that short stages load all alike
@@ -755,14 +742,14 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
         }
         if (cur.live) cur.live = __all_sync(0xffffffffu, tc::wait_phase(full0 + 8u * s, ph, p.fault));
         if (qi * F::QUARTER < values) {
-            const uint32_t aux = ring + (uint32_t)q.stages * WEIGHT_BYTES + (uint32_t)s * q.aux_bytes;
+            const uint32_t aux = aux0 + (uint32_t)s * q.aux_bytes;
             const uint32_t w0 = ring + (uint32_t)(s * WEIGHT_BYTES + (qi >> 1) * 2 * BOX_BYTES + (16 * half + rho) * 128);
             const int c16 = 4 * (qi & 1);                    // of the row's 16-byte chunks, this quarter's first
             const int left = (values - qi * F::QUARTER + 31) / 32;     // blocks of 32 in this quarter, at least
             uint32_t act[NT];
 #pragma unroll
             for (int c = 0; c < NT; ++c)
-                act[c] = aux + q.acts_at + (uint32_t)(col[c] * F::ACT_PITCH + qi * F::QUARTER * 2 + 16 * t);
+                act[c] = aux + q.acts_at + (uint32_t)(col[c] * F::RECORD + qi * F::QUARTER * 2 + 16 * t);
 
             if constexpr (FMT == kMx) {
                 // four blocks of 32; a lane holds values 8 t .. 8 t + 7 of each
@@ -782,8 +769,8 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
                 if constexpr (WHICH == 1) {
 #pragma unroll
                     for (int c = 0; c < NT; ++c) {
-                        const uint32_t pa = aux + q.pows_at + (uint32_t)(col[c] * F::POW_PITCH * 4);
-                        const float inv = as_f32(lds32(pa + F::BLOCKS * 4));
+                        const uint32_t pa = aux + q.acts_at + (uint32_t)(col[c] * F::RECORD + F::POWERS);
+                        const float inv = as_f32(lds32(aux + q.inverse_at + 4u * col[c]));
                         lds_pairs(pa + 16u * qi, ratio[c][0], ratio[c][1]);
                         ratio[c][0] = mul2(ratio[c][0], pk(inv, inv));
                         ratio[c][1] = mul2(ratio[c][1], pk(inv, inv));
@@ -831,9 +818,9 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
 #pragma unroll
                     for (int j = 0; j < PIECES; ++j) bf[c][j] = lds128(act[c] + 64u * j);
                     if constexpr (WHICH == 1) {
-                        const uint32_t pa = aux + q.pows_at + (uint32_t)(col[c] * F::POW_PITCH * 4);
+                        const uint32_t pa = aux + q.acts_at + (uint32_t)(col[c] * F::RECORD + F::POWERS);
                         const int block = FMT == kNv ? 4 * qi + t : 2 * qi + (t >> 1);
-                        const float r = __fmul_rn(as_f32(lds32(pa + 4u * block)), as_f32(lds32(pa + F::BLOCKS * 4)));
+                        const float r = __fmul_rn(as_f32(lds32(pa + 4u * block)), as_f32(lds32(aux + q.inverse_at + 4u * col[c])));
                         const uint32_t m = f16x2(r, r);
 #pragma unroll
                         for (int j = 0; j < PIECES; ++j) {
@@ -900,121 +887,136 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
     }
 }
 
-// An item from its products to h (WHICH 0) or to the pairs' results (1).
-template <int FMT, int NT, int WHICH>
-__device__ __forceinline__ void whole_item(const Params& p, const Shared& sh, uint32_t ring, float* buf, const Phase& f,
-                                           int it, bool wait_first, Cursor& cur)
-{
-    constexpr int PITCH = 8 * NT + 1;                        // of the partial sums, floats
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int grp = it / f.tiles, tile = it - grp * f.tiles;
-    const int e = sh.g_expert[grp], n = sh.g_count[grp], row0 = e * f.rows + tile * f.step;
-    const uint16_t* list = sh.list + sh.g_first[grp];
-    const float gs = FMT == kNv && f.m->gscale ? __ldg(f.m->gscale + e * f.m->gstride) : 1.0f;
-    // the powers of the columns that this thread will write, on their way while the products run
-    float pow[NT] = {};
-#pragma unroll
-    for (int k = 0; k < NT; ++k) {
-        const int c = WHICH == 0 ? warp : tid / TILE + 8 * k;
-        if (c < n) {
-            if (WHICH == 0) {
-                if (k == 0) pow[0] = __ldcg(p.xpow + list[c] / p.top_k);
-            } else {
-                float inv;
-                power_of(__ldcg(p.hmax + list[c]), pow[k], inv);
-            }
-        }
+// A place in the CTA's sequence of buffers of partial sums.
+struct Buffers {
+    int n, at;
+    uint32_t phase;
+    __device__ __forceinline__ void next()
+    {
+        if (++at == n) at = 0, phase ^= 1u;
     }
-    float acc[2][NT][4] = {};
-    item<FMT, NT, WHICH>(p, sh.plan, ring, smem_of(sh.full), smem_of(sh.empty), f, row0, n, cur, acc);
+};
 
-    const int g = lane >> 2, t = lane & 3, half = (warp >> 2) & 1;
+// The product warps' part of one phase.
+template <int FMT, int NT, int WHICH>
+__device__ __forceinline__ void item_products(const Params& p, const Shared& sh, uint32_t ring, float* red, const Phase& f,
+                                              int row0, int n, Cursor& cur, Buffers& buf)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float acc[2][NT][4] = {};
+    item<FMT, NT, WHICH>(p, sh.plan, ring, f, row0, n, cur, acc);
+
+    const int g = lane >> 2, t = lane & 3, half = (warp >> 2) & 1, pitch = sh.plan.pitch;
     const int slice = (warp >> 3) * 4 + (warp & 3), rho = (g >> 1) | ((g & 1) << 2);
-    if (wait_first) consumers_sync();                        // the last item's readers are done
+    if (cur.live) cur.live = __all_sync(0xffffffffu, tc::wait_phase(smem_of(&sh.summed[buf.at]), buf.phase ^ 1u, p.fault));
+    float* to = red + (buf.at * SLICES * TILE + slice * TILE + 16 * half + rho) * pitch + 2 * t;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int c = 0; c < NT; ++c)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                buf[(slice * TILE + 32 * i + 16 * half + rho + 8 * (j >> 1)) * PITCH + 8 * c + 2 * t + (j & 1)] =
-                    acc[i][c][j];
-    consumers_sync();
-    if (WHICH == 0) {
-        // a warp per pair: 32 consecutive values of h share a power of two
-        const int c = warp;
-        if (c < n) {
+            for (int j = 0; j < 4; ++j) to[(32 * i + 8 * (j >> 1)) * pitch + 8 * c + (j & 1)] = acc[i][c][j];
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(smem_of(&sh.summable[buf.at]));
+    buf.next();
+}
+
+template <int FMT, int WHICH>
+__device__ __forceinline__ void multiply(const Params& p, const Shared& sh, uint32_t ring, float* red, Cursor& cur, Buffers& buf)
+{
+    const Phase f = phase_of(p, sh.plan, WHICH);
+    for (int it = f.first; it < f.items; it += gridDim.x) {
+        const int grp = it / f.tiles, n = sh.g_count[grp];
+        const int row0 = sh.g_expert[grp] * f.rows + (it - grp * f.tiles) * f.step;
+        if (n > 8)
+            item_products<FMT, 2, WHICH>(p, sh, ring, red, f, row0, n, cur, buf);
+        else
+            item_products<FMT, 1, WHICH>(p, sh, ring, red, f, row0, n, cur, buf);
+    }
+}
+
+// The summing warps' part: the eight slices of k, in order, to h (WHICH 0) or
+// to the pairs' results (1), beside the next item's products.
+template <int FMT, int WHICH>
+__device__ __forceinline__ void add_slices(const Params& p, const Shared& sh, const float* red, Buffers& buf, bool& live)
+{
+    using F = Format<FMT>;
+    const Phase f = phase_of(p, sh.plan, WHICH);
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - (CONSUMERS + 1 + AUX_WARPS + SPARE_WARPS), pitch = sh.plan.pitch;
+    for (int it = f.first; it < f.items; it += gridDim.x, buf.next()) {
+        const int grp = it / f.tiles, tile = it - grp * f.tiles, e = sh.g_expert[grp], n = sh.g_count[grp];
+        const uint16_t* list = sh.list + sh.g_first[grp];
+        const float gs = FMT == kNv && f.m->gscale ? __ldg(f.m->gscale + e * f.m->gstride) : 1.0f;
+        float pow = 0.0f, inv;                               // lane c: of column c
+        if (lane < n) {
+            if (WHICH == 0)
+                pow = __ldcg(p.xpow + list[lane] / p.top_k);
+            else
+                power_of(__ldcg(p.hmax + list[lane]), pow, inv);
+        }
+        if (live) live = __all_sync(0xffffffffu, tc::wait_phase(smem_of(&sh.summable[buf.at]), buf.phase, p.fault));
+        const float* from = red + (buf.at * SLICES * TILE + lane) * pitch;
+        // a warp per pair, a lane for rows l and l + 32
+        for (int c = warp; c < n; c += SUM_WARPS) {
             float a = 0.0f, b = 0.0f;
 #pragma unroll
             for (int k = 0; k < SLICES; ++k) {
-                a += buf[(k * TILE + lane) * PITCH + c];
-                b += buf[(k * TILE + 32 + lane) * PITCH + c];
+                a += from[k * TILE * pitch + c];
+                b += from[(k * TILE + 32) * pitch + c];
             }
-            a = __fmul_rn(__fmul_rn(a, gs), pow[0]);
-            b = __fmul_rn(__fmul_rn(b, gs), pow[0]);
-            const float v = __fmul_rn(__fdiv_rn(a, 1.0f + expf(-a)), b);
-            const uint32_t top = __reduce_max_sync(0xffffffffu, finite_bits(v));
-            float own, inv;
-            power_of(top, own, inv);
-            const int pair = list[c];
-            __half* h = p.h + (int64_t)pair * p.ip;
-            float* hpow = p.hpow + (int64_t)pair * (p.ip / 32);
-            h[place<FMT>(tile * 32 + lane)] = __float2half_rn(__fmul_rn(v, inv));
-            if (lane == 0) {
-                hpow[tile] = own;
-                atomicMax(p.hmax + pair, top);
-            }
-            if (tile == f.tiles - 1)                         // zeros to the end of the padded row
-                for (int k = tile + 1; k < p.ip / 32; ++k) {
-                    h[place<FMT>(k * 32 + lane)] = __float2half_rn(0.0f);
-                    if (lane == 0) hpow[k] = 0.0f;
+            const float pw = __shfl_sync(0xffffffffu, pow, c);
+            a = __fmul_rn(__fmul_rn(a, gs), pw);
+            b = __fmul_rn(__fmul_rn(b, gs), pw);
+            const int64_t pair = list[c];
+            if (WHICH == 0) {
+                // 32 consecutive values of h share a power of two
+                const float v = __fmul_rn(__fdiv_rn(a, 1.0f + expf(-a)), b);
+                const uint32_t top = __reduce_max_sync(0xffffffffu, finite_bits(v));
+                float own;
+                power_of(top, own, inv);
+                uint8_t* rec = p.h + (pair * p.hstages + tile / F::BLOCKS) * F::RECORD;
+                const int block = tile % F::BLOCKS;
+                *reinterpret_cast<__half*>(rec + 2 * place<FMT>(block * 32 + lane)) = __float2half_rn(__fmul_rn(v, inv));
+                if (lane == 0) {
+                    *reinterpret_cast<float*>(rec + F::POWERS + 4 * block) = own;
+                    atomicMax(p.hmax + pair, top);
                 }
-        }
-    } else {
-        const int r = tid & (TILE - 1);
-        if (tile * TILE + r < p.hidden) {
-#pragma unroll
-            for (int k = 0; k < NT; ++k) {
-                const int c = tid / TILE + 8 * k;
-                if (c < n) {
-                    float a = 0.0f;
-#pragma unroll
-                    for (int l = 0; l < SLICES; ++l) a += buf[(l * TILE + r) * PITCH + c];
-                    p.o[(int64_t)list[c] * p.hidden + tile * TILE + r] = __fmul_rn(__fmul_rn(a, gs), pow[k]);
-                }
+                if (tile == f.tiles - 1)                     // zeros to the end of the last record
+                    for (int k = block + 1; k < F::BLOCKS; ++k) {
+                        *reinterpret_cast<__half*>(rec + 2 * place<FMT>(k * 32 + lane)) = __float2half_rn(0.0f);
+                        if (lane == 0) *reinterpret_cast<float*>(rec + F::POWERS + 4 * k) = 0.0f;
+                    }
+            } else {
+                float* o = p.o + pair * p.hidden + tile * TILE + lane;
+                o[0] = a;
+                if (tile * TILE + 32 < p.hidden) o[32] = b;
             }
         }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(smem_of(&sh.summed[buf.at]));
     }
 }
 
-// The consumer warps' part of one phase.
-template <int FMT, int WHICH>
-__device__ void multiply(const Params& p, const Shared& sh, uint32_t ring, float* red, Cursor& cur)
+// All of this CTA's summing warps have stored: count it.
+__device__ __forceinline__ void sums_count(unsigned int* counter)
 {
-    const Phase f = phase_of(p, sh.plan, WHICH);
-    bool wide_before = true;
-    int turn = 0;
-    for (int it = f.first; it < f.items; it += gridDim.x) {
-        // items of up to 8 columns alternate between two buffers and need no wait for the readers of the one before
-        const bool wide = sh.g_count[it / f.tiles] > 8;
-        if (wide) {
-            whole_item<FMT, 2, WHICH>(p, sh, ring, red, f, it, true, cur);
-        } else {
-            whole_item<FMT, 1, WHICH>(p, sh, ring, red + turn * (SLICES * TILE * 9), f, it, wide_before, cur);
-            turn ^= 1;
-        }
-        wide_before = wide;
-    }
-}
-
-// All of this CTA's consumer warps have stored: count it.
-__device__ __forceinline__ void consumers_count(unsigned int* counter)
-{
-    consumers_sync();
-    if (threadIdx.x == 0) {
+    sums_sync();
+    if (threadIdx.x == 32 * (CONSUMERS + 1 + AUX_WARPS + SPARE_WARPS)) {
         __threadfence();
         atomicAdd(counter, 1u);
     }
+}
+
+// All threads of all CTAs, for the n-th time.
+__device__ __forceinline__ void all_ctas(const Params& p, unsigned int n)
+{
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        atomicAdd(&p.ctl->start, 1u);
+        spin(&p.ctl->start, n * gridDim.x, p.fault);
+    }
+    __syncthreads();
 }
 
 template <int FMT>
@@ -1028,53 +1030,69 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(const __grid_constant__
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < MAX_STAGES; ++i) {
-            // the weights' bytes, the lanes that copy scale bytes and activations, and a lane for each warp of these
-            tc::mbar_init(smem_of(&sh.full[i]), 1u + (FMT == kF8 ? 0u : 32u) + 33u * ACT_WARPS);
+            // the weights' bytes; the lanes that copy scale bytes; the records' bytes
+            tc::mbar_init(smem_of(&sh.full[i]), 1u + (FMT == kF8 ? 0u : 32u) + 1u);
             tc::mbar_init(smem_of(&sh.empty[i]), (uint32_t)CONSUMERS / 2u);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(smem_of(&sh.summable[i]), (uint32_t)CONSUMERS);
+            tc::mbar_init(smem_of(&sh.summed[i]), (uint32_t)SUM_WARPS);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     convert_x<FMT>(p, reinterpret_cast<unsigned int*>(red));
     if (p.router) route_logits(p);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        __threadfence();
-        atomicAdd(&p.ctl->start, 1u);
-        spin(&p.ctl->start, gridDim.x, p.fault);
-    }
-    __syncthreads();
-    if (p.router) {
+    all_ctas(p, 1u);
+    // A few tokens every CTA chooses for by itself.  More are shared out, a CTA a
+    // token: another wait for all CTAs, 1.3 us, but every CTA reading all logits
+    // took 15 us for 64 tokens of 64 experts.
+    const bool shared_out = p.router && p.tokens > 8;
+    if (p.router && (!shared_out || warp == 0)) {
+        const int first = shared_out ? (int)blockIdx.x : warp, step = shared_out ? (int)gridDim.x : THREADS / 32;
+        const bool tell = shared_out || blockIdx.x == 0;
         if (p.experts <= 32)
-            choose<1>(p, sh);
+            choose<1>(p, sh, first, step, tell);
         else if (p.experts <= 128)
-            choose<4>(p, sh);
+            choose<4>(p, sh, first, step, tell);
         else
-            choose<MAX_EXPERTS / 32>(p, sh);
-    } else {
+            choose<MAX_EXPERTS / 32>(p, sh, first, step, tell);
+    }
+    if (shared_out) all_ctas(p, 2u);
+    if (shared_out || !p.router) {
         for (int i = threadIdx.x; i < p.tokens * p.top_k; i += THREADS) {
-            const int e = p.ids[i];
+            const int e = __ldcg(p.ids + i);
             sh.id[i] = (unsigned)e < (unsigned)p.experts ? (uint16_t)e : (uint16_t)NONE;
-            sh.w[i] = p.weights[i];
+            sh.w[i] = __ldcg(p.weights + i);
         }
     }
     __syncthreads();
     make_plan<FMT>(p, sh);
 
     if (warp < CONSUMERS) {
-        Cursor cur{0, 0u, 0u, true};
-        multiply<FMT, 0>(p, sh, ring, red, cur);
-        consumers_count(&p.ctl->h_done);
-        // the pairs' maxima are read directly, not through a stage
-        if ((threadIdx.x & 31) == 0) cur.live = spin(&p.ctl->h_done, gridDim.x, p.fault) && cur.live;
-        cur.live = __all_sync(0xffffffffu, cur.live);
-        multiply<FMT, 1>(p, sh, ring, red, cur);
-        consumers_count(&p.ctl->o_done);
-    } else if (warp == CONSUMERS) {
-        stream_weights<FMT>(p, sh, ring);
-    } else if (warp == CONSUMERS + 1) {
-        if constexpr (FMT != kF8) stream_scales<FMT>(p, sh, ring);
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_PRODUCTS));
+        Cursor cur{smem_of(sh.full), smem_of(sh.empty), sh.plan.stages, 0, 0u, 0u, true};
+        Buffers buf{sh.plan.buffers, 0, 0u};
+        multiply<FMT, 0>(p, sh, ring, red, cur, buf);
+        multiply<FMT, 1>(p, sh, ring, red, cur, buf);
+    } else if (warp < CONSUMERS + 1 + AUX_WARPS + SPARE_WARPS) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHERS));
+        if (warp == CONSUMERS) {
+            if ((threadIdx.x & 31) == 0) stream_weights<FMT>(p, sh, ring);
+            __syncwarp();
+        } else if (warp < CONSUMERS + 1 + AUX_WARPS) {
+            stream_aux<FMT>(p, sh, ring, warp - CONSUMERS - 1);
+        }
     } else {
-        stream_activations<FMT>(p, sh, ring, warp - CONSUMERS - 2);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHERS));
+        Buffers buf{sh.plan.buffers, 0, 0u};
+        bool live = true;
+        add_slices<FMT, 0>(p, sh, red, buf, live);
+        sums_count(&p.ctl->h_done);
+        // the pairs' maxima are read directly, not through a stage
+        if (threadIdx.x == 32 * (CONSUMERS + 1 + AUX_WARPS + SPARE_WARPS)) spin(&p.ctl->h_done, gridDim.x, p.fault);
+        sums_sync();
+        add_slices<FMT, 1>(p, sh, red, buf, live);
+        sums_count(&p.ctl->o_done);
     }
     __syncthreads();
     if (threadIdx.x == 0) spin(&p.ctl->o_done, gridDim.x, p.fault);
@@ -1110,23 +1128,27 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(const __grid_constant__
 }
 
 // ---------------------------------------------------------------- host
-int64_t padded(int64_t v) { return (v + 127) & ~(int64_t)127; }
+// Stages and bytes of a row of records (Format::VALUES, RECORD).
+int64_t stages_of(int64_t values, int fmt) { return fmt == kF8 ? (values + 255) / 256 : (values + 511) / 512; }
+int64_t record_bytes(int fmt) { return fmt == kF8 ? Format<kF8>::RECORD : Format<kNv>::RECORD; }
+static_assert(Format<kF8>::VALUES == 256 && Format<kNv>::VALUES == 512 && Format<kMx>::VALUES == 512 &&
+                  Format<kMx>::RECORD == Format<kNv>::RECORD,
+              "stages_of and record_bytes");
 
 struct Layout {
-    size_t logits, xs, xpow, h, hpow, hmax, o, total;
+    size_t logits, xs, xpow, h, hmax, o, total;
 };
 
-Layout layout(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k)
+Layout layout(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k, int fmt)
 {
     auto up = [](int64_t v) { return (size_t)((v + 255) & ~(int64_t)255); };
-    const int64_t pairs = tokens * top_k;
+    const int64_t pairs = tokens * top_k, rec = record_bytes(fmt);
     Layout l;
     l.logits = 256;
     l.xs = l.logits + up(8 * tokens * experts * 4);
-    l.xpow = l.xs + up(tokens * padded(hidden) * 2);
+    l.xpow = l.xs + up(tokens * stages_of(hidden, fmt) * rec);
     l.h = l.xpow + up(tokens * 4);
-    l.hpow = l.h + up(pairs * padded(inter) * 2);
-    l.hmax = l.hpow + up(pairs * padded(inter) / 32 * 4);
+    l.hmax = l.h + up(pairs * stages_of(inter, fmt) * rec);
     l.o = l.hmax + up(pairs * 4);
     l.total = l.o + up(pairs * hidden * 4);
     return l;
@@ -1165,7 +1187,10 @@ int launch(Params& p, cudaStream_t s)
 extern "C" size_t fp4q_moe_workspace_size(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k)
 {
     if (fp4q::moe::check(tokens, hidden, inter, experts, top_k) != FP4Q_OK) return 0;
-    return fp4q::moe::layout(tokens, hidden, inter, experts, top_k).total;
+    // a record per 512 FP4 values or two per 512 E4M3 values: room for either
+    const size_t a = fp4q::moe::layout(tokens, hidden, inter, experts, top_k, fp4q::moe::kF8).total;
+    const size_t b = fp4q::moe::layout(tokens, hidden, inter, experts, top_k, fp4q::moe::kNv).total;
+    return a > b ? a : b;
 }
 
 extern "C" int fp4q_moe(const void* x, int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k,
@@ -1192,8 +1217,8 @@ extern "C" int fp4q_moe(const void* x, int64_t tokens, int64_t hidden, int64_t i
     if (misaligned(x, 16) || (router && misaligned(router, 16)) || misaligned(ids, 4) || misaligned(weights, 4) ||
         misaligned(y, 16) || misaligned(workspace, 16))
         return FP4Q_ERR_ALIGN;
-    const Layout l = layout(tokens, hidden, inter, experts, top_k);
-    if (ws_bytes < l.total) return FP4Q_ERR_WORKSPACE;
+    const Layout l = layout(tokens, hidden, inter, experts, top_k, fmt);
+    if (ws_bytes < fp4q_moe_workspace_size(tokens, hidden, inter, experts, top_k)) return FP4Q_ERR_WORKSPACE;
 
     Params p;
     memset(&p, 0, sizeof(p));
@@ -1215,10 +1240,9 @@ extern "C" int fp4q_moe(const void* x, int64_t tokens, int64_t hidden, int64_t i
     char* ws = static_cast<char*>(workspace);
     p.ctl = reinterpret_cast<Control*>(ws);
     p.logits = reinterpret_cast<float*>(ws + l.logits);
-    p.xs = reinterpret_cast<__half*>(ws + l.xs);
+    p.xs = reinterpret_cast<uint8_t*>(ws + l.xs);
     p.xpow = reinterpret_cast<float*>(ws + l.xpow);
-    p.h = reinterpret_cast<__half*>(ws + l.h);
-    p.hpow = reinterpret_cast<float*>(ws + l.hpow);
+    p.h = reinterpret_cast<uint8_t*>(ws + l.h);
     p.hmax = reinterpret_cast<unsigned int*>(ws + l.hmax);
     p.o = reinterpret_cast<float*>(ws + l.o);
     p.tokens = (int)tokens;
@@ -1227,8 +1251,8 @@ extern "C" int fp4q_moe(const void* x, int64_t tokens, int64_t hidden, int64_t i
     p.experts = (int)experts;
     p.top_k = (int)top_k;
     p.normalize = normalize != 0;
-    p.hp = (int)padded(hidden);
-    p.ip = (int)padded(inter);
+    p.xstages = (int)stages_of(hidden, fmt);
+    p.hstages = (int)stages_of(inter, fmt);
     p.fault = device_fault_word();
     if (!p.fault) return FP4Q_ERR_CUDA;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
@@ -1236,3 +1260,4 @@ extern "C" int fp4q_moe(const void* x, int64_t tokens, int64_t hidden, int64_t i
     if (fmt == kNv) return launch<kNv>(p, cs);
     return launch<kF8>(p, cs);
 }
+
