@@ -9,7 +9,6 @@ library is missing, the first call raises ImportError.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -125,29 +124,42 @@ def _need_cuda(*ts):
             raise ValueError("fp4q tensors must live on a CUDA device")
 
 
-def _on(device, stream, *ts):
-    """Checks that every given tensor lives on `device` (a CUDA device), and
-    returns a context in which that device, and the given stream, are current:
-    what a call allocates or copies is then ordered with its kernels."""
-    if device.type != "cuda":
-        raise ValueError("fp4q tensors must live on a CUDA device")
+def _one_device(*ts) -> None:
+    """Checks that the given tensors live on the current CUDA device."""
+    index = torch._C._cuda_getDevice()
     for t in ts:
-        if t is not None and t.device != device:
-            raise ValueError("fp4q tensors of one call must live on one device")
-    if stream is not None:
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device) if stream else torch.cuda.default_stream(device)
-        return torch.cuda.stream(stream)
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+        if t is not None and t.get_device() != index:
+            raise ValueError("fp4q tensors of one call must live on one CUDA device")
+
+
+def _elsewhere(t: torch.Tensor, stream) -> bool:
+    """Whether a call has to be made under another device or stream than the current ones."""
+    return stream is not None or (t.is_cuda and t.get_device() != torch._C._cuda_getDevice())
+
+
+def _on(t: torch.Tensor, stream):
+    """A context in which t's device, and the given stream, are current: what a
+    call allocates or copies is then ordered with its kernels."""
+    if not t.is_cuda:
+        raise ValueError("fp4q tensors must live on a CUDA device")
+    if stream is None:
+        return torch.cuda.device(t.device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), t.device) if stream else torch.cuda.default_stream(t.device)
+    if stream.device != t.device:
+        raise ValueError("the stream must be one of the tensors' device")
+    return torch.cuda.stream(stream)
+
+
+def _current_stream(t: torch.Tensor) -> int:
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _out(t: Optional[torch.Tensor], shape, dtype, device, name: str) -> torch.Tensor:
     """A given output, checked, or a new one."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
     return t
 
@@ -279,28 +291,30 @@ def fp4q_f8_quantize(x: torch.Tensor, grain="row", codes: Optional[torch.Tensor]
     128 x 128 tile (grain "tile", weights)."""
     if x.dtype != torch.bfloat16 or x.dim() != 2:
         raise ValueError("x must be a 2-D bf16 tensor")
+    if _elsewhere(x, stream):
+        with _on(x, stream):
+            return fp4q_f8_quantize(x, grain, codes, scales)
+    _one_device(x, codes, scales)
     grain = {"row": FP4Q_F8_ROW, "tile": FP4Q_F8_TILE}[grain.lower()] if isinstance(grain, str) else int(grain)
-    dev = x.device
-    with _on(dev, stream, codes, scales):
-        x = x.contiguous()
-        rows, cols = x.shape
-        codes = _out(codes, (rows, cols), torch.float8_e4m3fn, dev, "codes")
-        scales = _out(scales, (rows if grain == FP4Q_F8_ROW else -(-rows // 128), -(-cols // 128)), torch.float32,
-                      dev, "scales")
-        st = lib().fp4q_f8_quantize(x.data_ptr(), rows, cols, grain, codes.data_ptr(), scales.data_ptr(),
-                                    torch.cuda.current_stream(dev).cuda_stream)
-    _check(st, "fp4q_f8_quantize")
+    x = x.contiguous()
+    rows, cols = x.shape
+    codes = _out(codes, (rows, cols), torch.float8_e4m3fn, x.device, "codes")
+    scales = _out(scales, (rows if grain == FP4Q_F8_ROW else -(-rows // 128), -(-cols // 128)), torch.float32,
+                  x.device, "scales")
+    _check(lib().fp4q_f8_quantize(x.data_ptr(), rows, cols, grain, codes.data_ptr(), scales.data_ptr(),
+                                  _current_stream(x)), "fp4q_f8_quantize")
     return codes, scales
 
 
-def _f8_operand(codes, scales, by_tiles: bool, name: str) -> None:
-    """Checks an operand of fp4q_f8_gemm: codes and scales of the shapes fp4q_f8_quantize gives."""
+def _f8_operand(codes, scales, by_tiles: bool, name: str) -> Tuple[int, int]:
+    """Checks an operand of fp4q_f8_gemm: codes and scales of the shapes fp4q_f8_quantize gives; its sizes."""
     if codes.dtype not in (torch.float8_e4m3fn, torch.uint8) or codes.dim() != 2:
         raise ValueError(f"codes_{name} must be a 2-D float8_e4m3fn (or uint8) tensor")
     rows, k = codes.shape
     want = (-(-rows // 128) if by_tiles else rows, -(-k // 128))
-    if scales.dtype != torch.float32 or tuple(scales.shape) != want:
+    if scales.dtype != torch.float32 or scales.shape != want:
         raise ValueError(f"scales_{name} must be a float32 tensor of shape {want}")
+    return rows, k
 
 
 def fp4q_f8_gemm(codes_a: torch.Tensor, scales_a: torch.Tensor, codes_b: torch.Tensor, scales_b: torch.Tensor,
@@ -308,22 +322,22 @@ def fp4q_f8_gemm(codes_a: torch.Tensor, scales_a: torch.Tensor, codes_b: torch.T
                  stream=None) -> torch.Tensor:
     """y = A B^T of two fp4q_f8_quantize operands, A [m, k] quantized by rows and B
     [n, k] by tiles; returns y [m, n] in bf16 or fp32."""
-    _f8_operand(codes_a, scales_a, False, "a")
-    _f8_operand(codes_b, scales_b, True, "b")
-    m, k = codes_a.shape
-    n = codes_b.shape[0]
-    if codes_b.shape[1] != k:
+    if _elsewhere(codes_a, stream):
+        with _on(codes_a, stream):
+            return fp4q_f8_gemm(codes_a, scales_a, codes_b, scales_b, out_dtype, y)
+    _one_device(codes_a, scales_a, codes_b, scales_b, y)
+    m, k = _f8_operand(codes_a, scales_a, False, "a")
+    n, kb = _f8_operand(codes_b, scales_b, True, "b")
+    if kb != k:
         raise ValueError("A and B must have the same k")
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
-    dev = codes_a.device
-    with _on(dev, stream, scales_a, codes_b, scales_b, y):
-        codes_a, scales_a, codes_b, scales_b = (t.contiguous() for t in (codes_a, scales_a, codes_b, scales_b))
-        y = _out(y, (m, n), out_dtype, dev, "y")
-        st = lib().fp4q_f8_gemm(codes_a.data_ptr(), scales_a.data_ptr(), m, codes_b.data_ptr(), scales_b.data_ptr(),
-                                n, k, FP4Q_OUT_F32 if out_dtype == torch.float32 else FP4Q_OUT_BF16, y.data_ptr(),
-                                torch.cuda.current_stream(dev).cuda_stream)
-    _check(st, "fp4q_f8_gemm")
+    codes_a, scales_a = codes_a.contiguous(), scales_a.contiguous()
+    codes_b, scales_b = codes_b.contiguous(), scales_b.contiguous()
+    y = _out(y, (m, n), out_dtype, codes_a.device, "y")
+    _check(lib().fp4q_f8_gemm(codes_a.data_ptr(), scales_a.data_ptr(), m, codes_b.data_ptr(), scales_b.data_ptr(),
+                              n, k, FP4Q_OUT_F32 if out_dtype == torch.float32 else FP4Q_OUT_BF16, y.data_ptr(),
+                              _current_stream(y)), "fp4q_f8_gemm")
     return y
 
 
@@ -685,35 +699,37 @@ def fp4q_moe(x: torch.Tensor, router: Optional[torch.Tensor], top_k: int, up, do
         raise ValueError("x must be a 2-D bf16 tensor")
     if fmt not in _MOE_FMT:
         raise ValueError(f"fmt must be one of {sorted(_MOE_FMT)}")
+    if _elsewhere(x, stream):
+        with _on(x, stream):
+            return fp4q_moe(x, router, top_k, up, down, fmt, normalize, ids, weights, y, workspace)
+    _one_device(x, router, ids, weights, y, workspace, *up, *down)
     tokens, hidden = x.shape
     inter = down[0].shape[-1] * (1 if fmt == "f8" else 2)
-    dev = x.device
+    x = x.contiguous()
     if router is not None:
         if router.dtype != torch.bfloat16 or router.dim() != 2 or router.shape[1] != hidden:
             raise ValueError("router must be a bf16 tensor [experts, hidden]")
+        router = router.contiguous()
         experts = router.shape[0]
     else:
         if ids is None or weights is None:
             raise ValueError("without a router, ids and weights must be given")
+        ids, weights = ids.contiguous(), weights.contiguous()
         experts = down[0].numel() // max(1, hidden * down[0].shape[-1])
-    with _on(dev, stream, router, ids, weights, y, workspace, *up, *down):
-        x = x.contiguous()
-        router = None if router is None else router.contiguous()
-        if router is None:
-            ids, weights = ids.contiguous(), weights.contiguous()
-        u = _moe_matrix(up, fmt, 2 * inter, hidden, experts, "up")
-        d = _moe_matrix(down, fmt, hidden, inter, experts, "down")
-        ids = _out(ids, (tokens, top_k), torch.int32, dev, "ids")
-        weights = _out(weights, (tokens, top_k), torch.float32, dev, "weights")
-        y = _out(y, (tokens, hidden), torch.bfloat16, dev, "y")
-        if workspace is None:
-            workspace = torch.zeros((max(1, fp4q_moe_workspace_size(tokens, hidden, inter, experts, top_k)),),
-                                    dtype=torch.uint8, device=dev)
-        st = lib().fp4q_moe(x.data_ptr(), tokens, hidden, inter, experts, top_k, _ptr(router), 1 if normalize else 0,
-                            _MOE_FMT[fmt][0], ctypes.addressof(u), ctypes.addressof(d), ids.data_ptr(),
-                            weights.data_ptr(), y.data_ptr(), workspace.data_ptr(),
-                            workspace.numel() * workspace.element_size(), torch.cuda.current_stream(dev).cuda_stream)
-    _check(st, "fp4q_moe")
+    u = _moe_matrix(up, fmt, 2 * inter, hidden, experts, "up")
+    d = _moe_matrix(down, fmt, hidden, inter, experts, "down")
+    ids = _out(ids, (tokens, top_k), torch.int32, x.device, "ids")
+    weights = _out(weights, (tokens, top_k), torch.float32, x.device, "weights")
+    y = _out(y, (tokens, hidden), torch.bfloat16, x.device, "y")
+    if workspace is None:
+        workspace = torch.zeros((max(1, fp4q_moe_workspace_size(tokens, hidden, inter, experts, top_k)),),
+                                dtype=torch.uint8, device=x.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _check(lib().fp4q_moe(x.data_ptr(), tokens, hidden, inter, experts, top_k, _ptr(router), 1 if normalize else 0,
+                          _MOE_FMT[fmt][0], ctypes.addressof(u), ctypes.addressof(d), ids.data_ptr(),
+                          weights.data_ptr(), y.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                          _current_stream(x)), "fp4q_moe")
     return y, ids, weights
 
 

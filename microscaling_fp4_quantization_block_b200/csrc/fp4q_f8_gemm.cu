@@ -278,6 +278,264 @@ int launch(Params& p, const uint8_t* b, int64_t k, cudaStream_t s)
     return cudaGetLastError() == cudaSuccess ? FP4Q_OK : FP4Q_ERR_CUDA;
 }
 
+// ---------------------------------------------------------------- few tokens
+// With few rows of A the product is bound by B's bytes (or, at a few hundred
+// rows, there are too few 128 x 128 tiles for the SMs), so B's rows take the
+// 128 lanes of the MMA, up to NTOK rows of A its columns, and k is split over
+// the CTAs of a cluster.  A lane of tensor memory is then a row of B: the
+// scales vary along the columns and come from shared memory, where the CTA has
+// multiplied fp32(sA sB) for its blocks beforehand.  At the end CTA r of the
+// cluster adds every CTA's sums of its share of the columns, in rank order,
+// through distributed shared memory: no workspace, no atomics, and 32 lanes
+// store 32 neighbouring columns of a row of y.
+template <int NTOK>
+struct Small {
+    static constexpr int B_BYTES = 128 * BK;
+    static constexpr int STAGE_BYTES = B_BYTES + NTOK * BK;
+    static constexpr int NSTAGE = NTOK == 16 ? 5 : 4;
+    static constexpr int NBUF = 4;
+    static constexpr uint32_t COLS = NBUF * NTOK;           // 64, 128, 256: two CTAs share an SM's 512
+    static constexpr int SCALE_BYTES = NTOK <= 32 ? 16384 : 12288;
+    static constexpr int MAX_KB = SCALE_BYTES / 4 / NTOK;   // blocks of k per CTA
+    static constexpr int SMEM_BYTES = 1024 + NSTAGE * STAGE_BYTES + SCALE_BYTES + 256;
+    static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
+    static_assert(NSTAGE * STAGE_BYTES >= NTOK * 128 * 4, "the partial sums reuse the ring");
+};
+constexpr int SMALL_THREADS = 32 * 6;
+
+struct SmallParams {
+    CUtensorMap ta;                 // A codes, box NTOK x 128
+    CUtensorMap tb;                 // B codes, box 128 x 128
+    const float* sa;
+    const float* sb;
+    void* y;
+    int64_t m, n, kb;
+    int f32, split;                 // CTAs per cluster
+    unsigned int* fault;
+};
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr)
+                 : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void store_one(const SmallParams& p, int64_t row, int64_t col, float v)
+{
+    if (p.f32)
+        static_cast<float*>(p.y)[row * p.n + col] = v;
+    else
+        static_cast<__nv_bfloat16*>(p.y)[row * p.n + col] = __float2bfloat16_rn(v);
+}
+
+template <int NTOK>
+__global__ void __launch_bounds__(SMALL_THREADS, 2) f8_gemm_small_kernel(const __grid_constant__ SmallParams p)
+{
+    using S = Small<NTOK>;
+    extern __shared__ __align__(1024) uint8_t smem_f8[];
+    const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_f8);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    const uint32_t scales = base + S::NSTAGE * S::STAGE_BYTES;
+    const uint32_t full0 = scales + S::SCALE_BYTES, empty0 = full0 + 8u * S::NSTAGE;
+    const uint32_t afull0 = empty0 + 8u * S::NSTAGE, aempty0 = afull0 + 8u * S::NBUF, slot = aempty0 + 8u * S::NBUF;
+    float* sums = reinterpret_cast<float*>(smem_f8 + (base - raw));          // over the ring, once it is done with
+    float* sc = reinterpret_cast<float*>(smem_f8 + (scales - raw));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // cluster c: 128 rows of B, NTOK rows of A; its CTA `rank`: blocks from k0 to k1
+    const int rank = (int)(blockIdx.x % (unsigned)p.split);
+    const int64_t tile = blockIdx.x / (unsigned)p.split, tiles_m = (p.m + NTOK - 1) / NTOK;
+    const int64_t m0 = (tile % tiles_m) * NTOK, n0 = (tile / tiles_m) * 128;
+    const int k0 = (int)(p.kb * rank / p.split), k1 = (int)(p.kb * (rank + 1) / p.split), nk = k1 - k0;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::NSTAGE; ++i) {
+            tc::mbar_init(full0 + 8u * i, 1u);
+            tc::mbar_init(empty0 + 8u * i, 1u);
+        }
+        for (int i = 0; i < S::NBUF; ++i) {
+            tc::mbar_init(afull0 + 8u * i, 1u);
+            tc::mbar_init(aempty0 + 8u * i, 4u);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tc::tmem_alloc(slot, S::COLS);
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    uint32_t tmem;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(slot) : "memory");
+
+    f32x2 acc[NTOK / 2];
+    if (warp == 0 && lane == 0) {
+        for (int i = 0, s = 0, ph = 1; i < nk; ++i) {
+            if (!tc::wait_phase(empty0 + 8u * s, (uint32_t)ph, p.fault)) break;
+            const uint32_t st = base + (uint32_t)(s * S::STAGE_BYTES), fb = full0 + 8u * s;
+            tc::mbar_expect_tx(fb, (uint32_t)S::STAGE_BYTES);
+            tc::tma_load_2d(st, &p.tb, (k0 + i) * BK, (int)n0, fb);
+            tc::tma_load_2d(st + S::B_BYTES, &p.ta, (k0 + i) * BK, (int)m0, fb);
+            if (++s == S::NSTAGE) s = 0, ph ^= 1;
+        }
+    } else if (warp == 1 && lane == 0) {
+        for (int i = 0, s = 0, ph = 0, b = 0, bph = 1; i < nk; ++i) {
+            if (!tc::wait_phase(aempty0 + 8u * b, (uint32_t)bph, p.fault) ||
+                !tc::wait_phase(full0 + 8u * s, (uint32_t)ph, p.fault))
+                break;
+            tc::tc_fence_after();
+            const uint32_t st = base + (uint32_t)(s * S::STAGE_BYTES);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                mma_f8(tmem + (uint32_t)(b * NTOK), tc::sw128_desc(st + 32u * kk),
+                       tc::sw128_desc(st + S::B_BYTES + 32u * kk), idesc(128, NTOK), kk > 0);
+            tc::mma_commit(empty0 + 8u * s);
+            tc::mma_commit(afull0 + 8u * b);
+            if (++s == S::NSTAGE) s = 0, ph ^= 1;
+            if (++b == S::NBUF) b = 0, bph ^= 1;
+        }
+    } else if (warp >= 2) {
+        const int q = warp & 3, tid = (int)threadIdx.x - 64;
+        const float* sb = p.sb + (n0 >> 7) * p.kb + k0;
+        for (int i = tid; i < NTOK * nk; i += 128) {
+            const int t = i / nk, b = i - t * nk;
+            sc[b * NTOK + t] = m0 + t < p.m ? __fmul_rn(__ldg(p.sa + (m0 + t) * p.kb + k0 + b), __ldg(sb + b)) : 0.0f;
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+        for (int j = 0; j < NTOK / 2; ++j) acc[j] = 0ull;
+        bool live = true;
+        for (int i = 0, b = 0, bph = 0; i < nk; ++i) {
+            if (live) live = __all_sync(0xffffffffu, tc::wait_phase(afull0 + 8u * b, (uint32_t)bph, p.fault));
+            tc::tc_fence_after();
+            const uint32_t row = scales + (uint32_t)(i * NTOK * 4);
+            constexpr int W = NTOK < 32 ? 16 : 32;
+#pragma unroll
+            for (int c = 0; c < NTOK / W; ++c) {
+                uint32_t v[32];
+                const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(b * NTOK + W * c);
+                if constexpr (W == 16)
+                    tmem_ld16(at, v);
+                else
+                    tc::tmem_ld32(at, v);
+                if (c == NTOK / W - 1) {
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(aempty0 + 8u * b);
+                }
+#pragma unroll
+                for (int j = 0; j < W / 4; ++j) {
+                    f32x2 s0, s1;
+                    lds_pairs(row + (uint32_t)((W * c + 4 * j) * 4), s0, s1);
+                    f32x2& a0 = acc[(W * c + 4 * j) / 2];
+                    f32x2& a1 = acc[(W * c + 4 * j) / 2 + 1];
+                    a0 = fma2(pk(as_f32(v[4 * j]), as_f32(v[4 * j + 1])), s0, a0);
+                    a1 = fma2(pk(as_f32(v[4 * j + 2]), as_f32(v[4 * j + 3])), s1, a1);
+                }
+            }
+            if (++b == S::NBUF) b = 0, bph ^= 1;
+        }
+        if (p.split == 1) {
+            const int64_t col = n0 + 32 * q + lane;
+            if (col < p.n)
+#pragma unroll
+                for (int j = 0; j < NTOK / 2; ++j) {
+                    float a, b;
+                    upk(acc[j], a, b);
+                    if (m0 + 2 * j < p.m) store_one(p, m0 + 2 * j, col, a);
+                    if (m0 + 2 * j + 1 < p.m) store_one(p, m0 + 2 * j + 1, col, b);
+                }
+        }
+    }
+    if (p.split > 1) {
+        const int share = NTOK / p.split, log_share = __ffs(share) - 1;      // columns that each CTA adds: powers of two
+        __syncwarp();
+        __syncthreads();                                     // the ring has been read: the commits were waited for
+        cluster_sync();
+        if (warp >= 2) {
+            const int r = 32 * (warp & 3) + lane;
+#pragma unroll
+            for (int j = 0; j < NTOK; ++j) {
+                float a, b;
+                upk(acc[j / 2], a, b);
+                const int to = j >> log_share;
+                uint32_t dst = (uint32_t)__cvta_generic_to_shared(sums + ((rank * share + (j & (share - 1))) * 128 + r));
+                asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(dst) : "r"(to));
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(j & 1 ? b : a) : "memory");
+            }
+        }
+        cluster_sync();
+        if (warp >= 2) {
+            const int r = 32 * (warp & 3) + lane;
+            if (n0 + r < p.n)
+                for (int j = 0; j < share; ++j) {
+                    const int64_t row = m0 + rank * share + j;
+                    if (row >= p.m) break;
+                    float a = 0.0f;
+                    for (int k = 0; k < p.split; ++k) a += sums[(k * share + j) * 128 + r];
+                    store_one(p, row, n0 + r, a);
+                }
+        }
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tmem, S::COLS);
+    }
+}
+
+// The few-token product in tiles of 128 x NTOK over clusters of `split` CTAs.
+template <int NTOK>
+int launch_small(const Params& g, const uint8_t* a, const uint8_t* b, int64_t k, int split, cudaStream_t s)
+{
+    SmallParams p;
+    memset(&p, 0, sizeof(p));
+    if (!make_byte_map(&p.ta, a, g.m, k, NTOK) || !make_byte_map(&p.tb, b, g.n, k, 128)) return FP4Q_ERR_CUDA;
+    p.sa = g.sa;
+    p.sb = g.sb;
+    p.y = g.y;
+    p.m = g.m;
+    p.n = g.n;
+    p.kb = g.kb;
+    p.f32 = g.f32;
+    p.split = split;
+    p.fault = g.fault;
+    resident_ctas((const void*)f8_gemm_small_kernel<NTOK>, Small<NTOK>::SMEM_BYTES, SMALL_THREADS);   // opts in to the shared memory
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(((g.m + NTOK - 1) / NTOK) * ((g.n + 127) / 128) * split));
+    cfg.blockDim = dim3((unsigned)SMALL_THREADS);
+    cfg.dynamicSmemBytes = Small<NTOK>::SMEM_BYTES;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, f8_gemm_small_kernel<NTOK>, p) == cudaSuccess ? FP4Q_OK : FP4Q_ERR_CUDA;
+}
+
+// CTAs per cluster for `tiles` tiles of kb blocks: the most (8 at most) that all
+// fit at two CTAs per SM and have two blocks each; 0 if a CTA's scales would not fit.
+int split_of(int64_t tiles, int64_t kb, int max_kb)
+{
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= 2 * 148 && kb >= 4 * split) split *= 2;
+    while (split < 8 && (kb + split - 1) / split > max_kb) split *= 2;
+    return (kb + split - 1) / split <= max_kb ? split : 0;
+}
+
 }  // namespace f8gemm
 }  // namespace fp4q
 
@@ -312,6 +570,16 @@ extern "C" int fp4q_f8_gemm(const uint8_t* codes_a, const float* scales_a, int64
     p.f32 = out_dtype == FP4Q_OUT_F32;
     p.fault = device_fault_word();
     if (!p.fault) return FP4Q_ERR_CUDA;
+    // Few rows of A, or few tiles: rows of A in tiles of 16 to 64, k split over clusters.
+    const int ntok = m <= 16 ? 16 : m <= 32 ? 32 : 64;
+    const int64_t tiles = ((m + ntok - 1) / ntok) * ((n + 127) / 128);
+    if (m <= 64 || tiles <= 2 * 148) {
+        const int max_kb = ntok == 16 ? f8gemm::Small<16>::MAX_KB : ntok == 32 ? f8gemm::Small<32>::MAX_KB : f8gemm::Small<64>::MAX_KB;
+        const int split = f8gemm::split_of(tiles, p.kb, max_kb);
+        if (split && ntok == 16) return f8gemm::launch_small<16>(p, codes_a, codes_b, k, split, s);
+        if (split && ntok == 32) return f8gemm::launch_small<32>(p, codes_a, codes_b, k, split, s);
+        if (split) return f8gemm::launch_small<64>(p, codes_a, codes_b, k, split, s);
+    }
     if (n > 128 && ((m + 127) / 128) * ((n + 255) / 256) >= 148) return f8gemm::launch<256>(p, codes_b, k, s);
     return f8gemm::launch<128>(p, codes_b, k, s);
 }
