@@ -296,7 +296,8 @@ struct Small {
     static constexpr int NBUF = 4;
     static constexpr uint32_t COLS = NBUF * NTOK;           // 64, 128, 256: two CTAs share an SM's 512
     static constexpr int SCALE_BYTES = NTOK <= 32 ? 16384 : 12288;
-    static constexpr int MAX_KB = SCALE_BYTES / 4 / NTOK;   // blocks of k per CTA
+    static constexpr int SCALE_PITCH = NTOK + 4;            // floats per block of k
+    static constexpr int MAX_KB = SCALE_BYTES / 4 / SCALE_PITCH;            // blocks of k per CTA
     static constexpr int SMEM_BYTES = 1024 + NSTAGE * STAGE_BYTES + SCALE_BYTES + 256;
     static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
     static_assert(NSTAGE * STAGE_BYTES >= NTOK * 128 * 4, "the partial sums reuse the ring");
@@ -403,11 +404,15 @@ __global__ void __launch_bounds__(SMALL_THREADS, 2) f8_gemm_small_kernel(const _
             if (++b == S::NBUF) b = 0, bph ^= 1;
         }
     } else if (warp >= 2) {
-        const int q = warp & 3, tid = (int)threadIdx.x - 64;
+        const int q = warp & 3;
         const float* sb = p.sb + (n0 >> 7) * p.kb + k0;
-        for (int i = tid; i < NTOK * nk; i += 128) {
-            const int t = i / nk, b = i - t * nk;
-            sc[b * NTOK + t] = m0 + t < p.m ? __fmul_rn(__ldg(p.sa + (m0 + t) * p.kb + k0 + b), __ldg(sb + b)) : 0.0f;
+        // 32 lanes a row of A, four rows at a time
+        for (int b = lane; b < nk; b += 32) {
+            const float v = __ldg(sb + b);
+            const float* a = p.sa + (m0 + q) * p.kb + k0 + b;
+#pragma unroll
+            for (int t = 0; t < NTOK / 4; ++t)
+                sc[b * S::SCALE_PITCH + 4 * t + q] = m0 + 4 * t + q < p.m ? __fmul_rn(__ldg(a + 4 * t * p.kb), v) : 0.0f;
         }
         asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
@@ -416,7 +421,7 @@ __global__ void __launch_bounds__(SMALL_THREADS, 2) f8_gemm_small_kernel(const _
         for (int i = 0, b = 0, bph = 0; i < nk; ++i) {
             if (live) live = __all_sync(0xffffffffu, tc::wait_phase(afull0 + 8u * b, (uint32_t)bph, p.fault));
             tc::tc_fence_after();
-            const uint32_t row = scales + (uint32_t)(i * NTOK * 4);
+            const uint32_t row = scales + (uint32_t)(i * S::SCALE_PITCH * 4);
             constexpr int W = NTOK < 32 ? 16 : 32;
 #pragma unroll
             for (int c = 0; c < NTOK / W; ++c) {
@@ -456,33 +461,37 @@ __global__ void __launch_bounds__(SMALL_THREADS, 2) f8_gemm_small_kernel(const _
         }
     }
     if (p.split > 1) {
-        const int share = NTOK / p.split, log_share = __ffs(share) - 1;      // columns that each CTA adds: powers of two
+        // columns that each CTA adds (a power of two, at least 2), kept [rank][column][row of B]: a warp's stores to
+        // another CTA are then 128 consecutive bytes (rows of `share` columns, 16 bytes a lane, took 1 us more)
+        const int share = NTOK / p.split, log_share = __ffs(share) - 1, r = 32 * (warp & 3) + lane;
         __syncwarp();
         __syncthreads();                                     // the ring has been read: the commits were waited for
         cluster_sync();
         if (warp >= 2) {
-            const int r = 32 * (warp & 3) + lane;
+            const uint32_t mine = (uint32_t)__cvta_generic_to_shared(sums + rank * share * 128 + r);
 #pragma unroll
             for (int j = 0; j < NTOK; ++j) {
                 float a, b;
                 upk(acc[j / 2], a, b);
-                const int to = j >> log_share;
-                uint32_t dst = (uint32_t)__cvta_generic_to_shared(sums + ((rank * share + (j & (share - 1))) * 128 + r));
-                asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(dst) : "r"(to));
+                uint32_t dst = mine + 512u * (uint32_t)(j & (share - 1));
+                asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(dst) : "r"(j >> log_share));
                 asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(j & 1 ? b : a) : "memory");
             }
         }
         cluster_sync();
-        if (warp >= 2) {
-            const int r = 32 * (warp & 3) + lane;
-            if (n0 + r < p.n)
-                for (int j = 0; j < share; ++j) {
-                    const int64_t row = m0 + rank * share + j;
-                    if (row >= p.m) break;
-                    float a = 0.0f;
-                    for (int k = 0; k < p.split; ++k) a += sums[(k * share + j) * 128 + r];
-                    store_one(p, row, n0 + r, a);
-                }
+        if (warp >= 2 && n0 + r < p.n) {
+            const int64_t row0 = m0 + rank * share;
+            for (int j = 0; j < share; j += 2) {
+                float a[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < p.split) {
+                        a[0] += sums[(k * share + j) * 128 + r];
+                        a[1] += sums[(k * share + j + 1) * 128 + r];
+                    }
+                if (row0 + j < p.m) store_one(p, row0 + j, n0 + r, a[0]);
+                if (row0 + j + 1 < p.m) store_one(p, row0 + j + 1, n0 + r, a[1]);
+            }
         }
     }
     tc::tc_fence_before();
