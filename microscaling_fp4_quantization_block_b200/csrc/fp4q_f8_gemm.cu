@@ -10,8 +10,10 @@
 // A persistent grid (one CTA per SM) walks the 128 x BN tiles of y; each tile
 // walks k in blocks of 128 bytes through a ring of shared-memory stages:
 //   warp 0, one thread: TMA loads of the A and B code tiles;
-//   warp 1: tensor memory; one thread issues a block's MMAs into the next of
-//     512 / BN accumulators, so block b + 1 runs while block b is drained;
+//   warps 1 and 2 (warp 1 also allocates tensor memory): one thread each issues
+//     every other block's MMAs into the next of 512 / BN accumulators, so block
+//     b + 1 runs while block b is drained.  One thread alone took 650 clocks a
+//     block for its two waits and two commits, more than the 512 of the MMAs;
 //   warps 4-11: two groups of four, each draining half the columns: a thread
 //     owns a row of y (a lane of tensor memory) and BN / 2 columns, the scale
 //     is one number per thread and block, and pairs of columns are scaled and
@@ -36,18 +38,21 @@ constexpr int BM = 128, BK = 128;
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 32 * (4 + EPI_WARPS);       // three warpgroups: control, two epilogue groups
 constexpr int REGS_CONTROL = 40, REGS_EPI = 232;    // 128 x 40 + 256 x 232 = 384 x 168, the launch's registers
+constexpr int ISSUERS = 2;                          // warps that issue MMAs, a block of k in turn
 constexpr uint32_t TMEM_COLS = 512;
 
 template <int BN>
 struct Shape {
     static constexpr int A_BYTES = BM * BK;
     static constexpr int STAGE_BYTES = A_BYTES + BN * BK;
-    static constexpr int NSTAGE = (208 * 1024) / STAGE_BYTES;
+    static constexpr int NSTAGE = ((208 * 1024) / STAGE_BYTES) & ~1;
     static constexpr int NBUF = (int)TMEM_COLS / BN;
     static constexpr int SMEM_BYTES = 1024 + NSTAGE * STAGE_BYTES + 256;
     static constexpr int HALF = BN / 2;                     // columns per epilogue group
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
     static_assert(16 * (NSTAGE + NBUF) + 8 <= 256, "barriers");
+    // a slot of either ring belongs to one issuer: a barrier's parity tells only neighbouring phases apart
+    static_assert(NSTAGE % ISSUERS == 0 && NBUF % ISSUERS == 0, "rings");
 };
 
 struct Params {
@@ -83,55 +88,117 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
     return r;
 }
 
+// tcgen05.ld without its wait, and the wait, which hands the registers on: what
+// uses them cannot be moved before it.
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+
+// acc += s * v, 32 columns.  Scalar fused multiply-adds: as packed pairs the
+// same sums took a quarter longer (8192 x 13824 x 5120: 781 against 618 us).
+__device__ __forceinline__ void add_scaled(float* acc, const uint32_t (&v)[32], float s)
+{
+#pragma unroll
+    for (int j = 0; j < 32; ++j) acc[j] = __fmaf_rn(as_f32(v[j]), s, acc[j]);
+}
+
 // One thread's HALF results of row r, from column c0.
 template <int HALF>
-__device__ __forceinline__ void store_row(const Params& p, int64_t r, int64_t c0, const f32x2 (&acc)[HALF / 2])
+__device__ __forceinline__ void store_row(const Params& p, int64_t r, int64_t c0, const float (&acc)[HALF])
 {
     if (r >= p.m || c0 >= p.n) return;
     if (p.f32) {
         float* dst = static_cast<float*>(p.y) + r * p.n + c0;
         if (c0 + HALF <= p.n && (reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
 #pragma unroll
-            for (int j = 0; j < HALF / 2; j += 4) {
-                float v[8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) upk(acc[j + i], v[2 * i], v[2 * i + 1]);
-                stg256(dst + 2 * j, as_u32(v[0]), as_u32(v[1]), as_u32(v[2]), as_u32(v[3]), as_u32(v[4]),
-                       as_u32(v[5]), as_u32(v[6]), as_u32(v[7]));
-            }
+            for (int j = 0; j < HALF; j += 8)
+                stg256(dst + j, as_u32(acc[j]), as_u32(acc[j + 1]), as_u32(acc[j + 2]), as_u32(acc[j + 3]),
+                       as_u32(acc[j + 4]), as_u32(acc[j + 5]), as_u32(acc[j + 6]), as_u32(acc[j + 7]));
         } else {
 #pragma unroll
-            for (int j = 0; j < HALF / 2; ++j) {
-                float a, b;
-                upk(acc[j], a, b);
-                if (c0 + 2 * j < p.n) dst[2 * j] = a;
-                if (c0 + 2 * j + 1 < p.n) dst[2 * j + 1] = b;
-            }
+            for (int j = 0; j < HALF; ++j)
+                if (c0 + j < p.n) dst[j] = acc[j];
         }
     } else {
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.y) + r * p.n + c0;
         if (c0 + HALF <= p.n && (reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
 #pragma unroll
-            for (int j = 0; j < HALF / 2; j += 8) {
+            for (int j = 0; j < HALF; j += 16) {
                 uint32_t v[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float a, b;
-                    upk(acc[j + i], a, b);
-                    v[i] = bf16x2(a, b);
-                }
-                stg256(dst + 2 * j, v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+                for (int i = 0; i < 8; ++i) v[i] = bf16x2(acc[j + 2 * i], acc[j + 2 * i + 1]);
+                stg256(dst + j, v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < HALF / 2; ++j) {
-                float a, b;
-                upk(acc[j], a, b);
-                if (c0 + 2 * j < p.n) dst[2 * j] = __float2bfloat16_rn(a);
-                if (c0 + 2 * j + 1 < p.n) dst[2 * j + 1] = __float2bfloat16_rn(b);
-            }
+            for (int j = 0; j < HALF; ++j)
+                if (c0 + j < p.n) dst[j] = __float2bfloat16_rn(acc[j]);
         }
     }
+}
+
+// An epilogue thread's part of a tile: row r, HALF columns from c0, over all
+// blocks of k; `release` hands an accumulator back.  False once a wait ran out.
+template <int BN, int NBUF, typename Release>
+__device__ __forceinline__ bool drain_tile(const Params& p, uint32_t tmem, uint32_t afull0, int half, int64_t r, int64_t c0,
+                                           int& b, uint32_t& bph, Release release)
+{
+    constexpr int HALF = BN / 2;
+    const int warp = threadIdx.x >> 5, q = warp & 3;
+    const float* sa = p.sa + (r < p.m ? r : p.m - 1) * p.kb;
+    const float* sb = p.sb + ((c0 < p.n ? c0 : p.n - 1) >> 7) * p.kb;
+    float acc[HALF];
+#pragma unroll
+    for (int j = 0; j < HALF; ++j) acc[j] = 0.0f;
+    float a1 = __ldg(sa), b1 = __ldg(sb);
+    for (int kt = 0; kt < (int)p.kb; ++kt) {
+        const float s = __fmul_rn(a1, b1);
+        const int nx = kt + 1 < (int)p.kb ? kt + 1 : kt;
+        a1 = __ldg(sa + nx);
+        b1 = __ldg(sb + nx);
+        const bool done = tc::wait_phase(afull0 + 8u * b, bph, p.fault);
+        if (!__all_sync(0xffffffffu, done)) return false;
+        tc::tc_fence_after();
+        // the next 32 columns are on their way while these are added
+        const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(b * BN + half * HALF);
+        uint32_t v[2][32];
+        tmem_ld32_issue(at, v[0]);
+#pragma unroll
+        for (int c = 0; c < HALF / 32; ++c) {
+            tmem_ld_wait(v[c & 1]);
+            if (c + 1 < HALF / 32) {
+                tmem_ld32_issue(at + 32u * (uint32_t)(c + 1), v[(c + 1) & 1]);
+            } else {
+                tc::tc_fence_before();
+                __syncwarp();
+                release(b);
+            }
+            add_scaled(acc + 32 * c, v[c & 1], s);
+        }
+        if (++b == NBUF) b = 0, bph ^= 1u;
+    }
+    store_row<HALF>(p, r, c0, acc);
+    return true;
 }
 
 template <int BN>
@@ -190,73 +257,39 @@ __global__ void __launch_bounds__(THREADS, 1) f8_gemm_kernel(const __grid_consta
                     if (++s == S::NSTAGE) s = 0, ph ^= 1u;
                 }
             }
-        } else if (warp == 1 && lane == 0) {
-            int s = 0, b = 0;
+        } else if (warp < 1 + ISSUERS && lane == 0) {
+            // blocks mine, mine + ISSUERS, ... of this CTA's sequence
+            const int mine = warp - 1;
+            int s = mine, b = mine;
             uint32_t ph = 0, bph = 1;
-            bool ok = true;
-            for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
-                for (int kt = 0; kt < (int)p.kb; ++kt) {
-                    if (!tc::wait_phase(aempty0 + 8u * b, bph, p.fault) || !tc::wait_phase(full0 + 8u * s, ph, p.fault)) {
-                        ok = false;
-                        break;
-                    }
-                    tc::tc_fence_after();
-                    const uint32_t st = base + (uint32_t)(s * S::STAGE_BYTES);
+            int64_t blocks = 0;
+            for (int64_t t = blockIdx.x; t < n_tiles; t += gridDim.x) blocks += p.kb;
+            for (int64_t i = mine; i < blocks; i += ISSUERS) {
+                if (!tc::wait_phase(aempty0 + 8u * b, bph, p.fault) || !tc::wait_phase(full0 + 8u * s, ph, p.fault)) break;
+                tc::tc_fence_after();
+                const uint32_t st = base + (uint32_t)(s * S::STAGE_BYTES);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_f8(tmem + (uint32_t)(b * BN), tc::sw128_desc(st + 32u * kk),
-                               tc::sw128_desc(st + S::A_BYTES + 32u * kk), idesc(BM, BN), kk > 0);
-                    tc::mma_commit(empty0 + 8u * s);
-                    tc::mma_commit(afull0 + 8u * b);
-                    if (++s == S::NSTAGE) s = 0, ph ^= 1u;
-                    if (++b == S::NBUF) b = 0, bph ^= 1u;
-                }
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_f8(tmem + (uint32_t)(b * BN), tc::sw128_desc(st + 32u * kk),
+                           tc::sw128_desc(st + S::A_BYTES + 32u * kk), idesc(BM, BN), kk > 0);
+                tc::mma_commit(empty0 + 8u * s);
+                tc::mma_commit(afull0 + 8u * b);
+                if ((s += ISSUERS) >= S::NSTAGE) s -= S::NSTAGE, ph ^= 1u;
+                if ((b += ISSUERS) >= S::NBUF) b -= S::NBUF, bph ^= 1u;
             }
         }
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPI));
-        const int q = warp & 3, half = (warp - 4) >> 2;
+        const int half = (warp - 4) >> 2;
         int b = 0;
         uint32_t bph = 0;
         bool ok = true;
         for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
-            const int64_t r = (t % tiles_m) * BM + 32 * q + lane;
-            const int64_t c0 = (t / tiles_m) * BN + half * S::HALF;
-            const float* sa = p.sa + (r < p.m ? r : p.m - 1) * p.kb;
-            const float* sb = p.sb + ((c0 < p.n ? c0 : p.n - 1) >> 7) * p.kb;
-            f32x2 acc[S::HALF / 2];
-#pragma unroll
-            for (int j = 0; j < S::HALF / 2; ++j) acc[j] = 0ull;
-            float a1 = __ldg(sa), b1 = __ldg(sb);
-            for (int kt = 0; kt < (int)p.kb; ++kt) {
-                const float s = __fmul_rn(a1, b1);
-                const int nx = kt + 1 < (int)p.kb ? kt + 1 : kt;
-                a1 = __ldg(sa + nx);
-                b1 = __ldg(sb + nx);
-                const bool done = tc::wait_phase(afull0 + 8u * b, bph, p.fault);
-                if (!__all_sync(0xffffffffu, done)) {
-                    ok = false;
-                    break;
-                }
-                tc::tc_fence_after();
-                const f32x2 s2 = pk(s, s);
-#pragma unroll
-                for (int c = 0; c < S::HALF / 32; ++c) {
-                    uint32_t v[32];
-                    tc::tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(b * BN + half * S::HALF + 32 * c), v);
-                    if (c == S::HALF / 32 - 1) {
-                        tc::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(aempty0 + 8u * b);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        acc[16 * c + j] = fma2(pk(as_f32(v[2 * j]), as_f32(v[2 * j + 1])), s2, acc[16 * c + j]);
-                }
-                if (++b == S::NBUF) b = 0, bph ^= 1u;
-            }
-            if (ok) store_row<S::HALF>(p, r, c0, acc);
+            ok = drain_tile<BN, S::NBUF>(p, tmem, afull0, half, (t % tiles_m) * BM + 32 * (warp & 3) + lane,
+                                         (t / tiles_m) * BN + half * S::HALF, b, bph, [&](int buf) {
+                                             if (lane == 0) tc::mbar_arrive(aempty0 + 8u * buf);
+                                         });
         }
     }
     tc::tc_fence_before();
@@ -266,6 +299,11 @@ __global__ void __launch_bounds__(THREADS, 1) f8_gemm_kernel(const __grid_consta
         tc::tc_fence_after();
         tc::tmem_dealloc(tmem, TMEM_COLS);
     }
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 template <int BN>
@@ -324,11 +362,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r)
                  : "r"(taddr)
                  : "memory");
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void store_one(const SmallParams& p, int64_t row, int64_t col, float v)
