@@ -45,9 +45,9 @@ template <int BN>
 struct Shape {
     static constexpr int A_BYTES = BM * BK;
     static constexpr int STAGE_BYTES = A_BYTES + BN * BK;
-    static constexpr int NSTAGE = ((208 * 1024) / STAGE_BYTES) & ~1;
+    static constexpr int NSTAGE = ((192 * 1024) / STAGE_BYTES) & ~1;
     static constexpr int NBUF = (int)TMEM_COLS / BN;
-    static constexpr int SMEM_BYTES = 1024 + NSTAGE * STAGE_BYTES + 256;
+    static constexpr int SMEM_BYTES = 1024 + NSTAGE * STAGE_BYTES + 256 + EPI_WARPS * 32 * 33 * 4;
     static constexpr int HALF = BN / 2;                     // columns per epilogue group
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
     static_assert(16 * (NSTAGE + NBUF) + 8 <= 256, "barriers");
@@ -122,38 +122,56 @@ __device__ __forceinline__ void add_scaled(float* acc, const uint32_t (&v)[32], 
     for (int j = 0; j < 32; ++j) acc[j] = __fmaf_rn(as_f32(v[j]), s, acc[j]);
 }
 
-// One thread's HALF results of row r, from column c0.
+// A warp's results: a thread has row r, HALF columns from c0.  Rows that 32-byte
+// stores fit (n a multiple of 16, or of 8 for fp32) go out as they are, a sector
+// a lane; others by way of the warp's corner of shared memory, 32 columns at a
+// time, so that the lanes store neighbouring columns of one row.
 template <int HALF>
-__device__ __forceinline__ void store_row(const Params& p, int64_t r, int64_t c0, const float (&acc)[HALF])
+__device__ __forceinline__ void store_rows(const Params& p, int64_t r, int64_t c0, const float (&acc)[HALF], float* corner)
 {
-    if (r >= p.m || c0 >= p.n) return;
-    if (p.f32) {
-        float* dst = static_cast<float*>(p.y) + r * p.n + c0;
-        if (c0 + HALF <= p.n && (reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
+    if (c0 >= p.n) return;
+    const int64_t at = r * p.n + c0;
+    const bool whole = c0 + HALF <= p.n;
+    if (p.f32 && whole && (p.n & 7) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 31u) == 0) {
+        if (r >= p.m) return;
+        float* dst = static_cast<float*>(p.y) + at;
 #pragma unroll
-            for (int j = 0; j < HALF; j += 8)
-                stg256(dst + j, as_u32(acc[j]), as_u32(acc[j + 1]), as_u32(acc[j + 2]), as_u32(acc[j + 3]),
-                       as_u32(acc[j + 4]), as_u32(acc[j + 5]), as_u32(acc[j + 6]), as_u32(acc[j + 7]));
-        } else {
+        for (int j = 0; j < HALF; j += 8)
+            stg256(dst + j, as_u32(acc[j]), as_u32(acc[j + 1]), as_u32(acc[j + 2]), as_u32(acc[j + 3]), as_u32(acc[j + 4]),
+                   as_u32(acc[j + 5]), as_u32(acc[j + 6]), as_u32(acc[j + 7]));
+    } else if (!p.f32 && whole && (p.n & 15) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 31u) == 0) {
+        if (r >= p.m) return;
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.y) + at;
 #pragma unroll
-            for (int j = 0; j < HALF; ++j)
-                if (c0 + j < p.n) dst[j] = acc[j];
+        for (int j = 0; j < HALF; j += 16) {
+            uint32_t v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = bf16x2(acc[j + 2 * i], acc[j + 2 * i + 1]);
+            stg256(dst + j, v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
         }
     } else {
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.y) + r * p.n + c0;
-        if (c0 + HALF <= p.n && (reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
+        const int lane = threadIdx.x & 31;
+        const int64_t r0 = r - lane;
 #pragma unroll
-            for (int j = 0; j < HALF; j += 16) {
-                uint32_t v[8];
+        for (int j = 0; j < HALF; j += 32) {
+            if (c0 + j >= p.n) break;
+            __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = bf16x2(acc[j + 2 * i], acc[j + 2 * i + 1]);
-                stg256(dst + j, v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < HALF; ++j)
-                if (c0 + j < p.n) dst[j] = __float2bfloat16_rn(acc[j]);
+            for (int i = 0; i < 32; ++i) corner[lane * 33 + i] = acc[j + i];
+            __syncwarp();
+            const int64_t col = c0 + j + lane;
+            const int rows = (int)(p.m - r0 < 32 ? p.m - r0 : 32);
+            if (col < p.n)
+#pragma unroll 4
+                for (int i = 0; i < rows; ++i) {
+                    const float v = corner[i * 33 + lane];
+                    if (p.f32)
+                        static_cast<float*>(p.y)[(r0 + i) * p.n + col] = v;
+                    else
+                        static_cast<__nv_bfloat16*>(p.y)[(r0 + i) * p.n + col] = __float2bfloat16_rn(v);
+                }
         }
+        __syncwarp();
     }
 }
 
@@ -161,7 +179,7 @@ __device__ __forceinline__ void store_row(const Params& p, int64_t r, int64_t c0
 // blocks of k; `release` hands an accumulator back.  False once a wait ran out.
 template <int BN, int NBUF, typename Release>
 __device__ __forceinline__ bool drain_tile(const Params& p, uint32_t tmem, uint32_t afull0, int half, int64_t r, int64_t c0,
-                                           int& b, uint32_t& bph, Release release)
+                                           int& b, uint32_t& bph, float* corner, Release release)
 {
     constexpr int HALF = BN / 2;
     const int warp = threadIdx.x >> 5, q = warp & 3;
@@ -197,7 +215,7 @@ __device__ __forceinline__ bool drain_tile(const Params& p, uint32_t tmem, uint3
         }
         if (++b == NBUF) b = 0, bph ^= 1u;
     }
-    store_row<HALF>(p, r, c0, acc);
+    store_rows<HALF>(p, r, c0, acc, corner);
     return true;
 }
 
@@ -282,12 +300,13 @@ __global__ void __launch_bounds__(THREADS, 1) f8_gemm_kernel(const __grid_consta
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPI));
         const int half = (warp - 4) >> 2;
+        float* corner = reinterpret_cast<float*>(smem_f8 + (base - raw) + S::NSTAGE * S::STAGE_BYTES + 256) + (warp - 4) * 32 * 33;
         int b = 0;
         uint32_t bph = 0;
         bool ok = true;
         for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
             ok = drain_tile<BN, S::NBUF>(p, tmem, afull0, half, (t % tiles_m) * BM + 32 * (warp & 3) + lane,
-                                         (t / tiles_m) * BN + half * S::HALF, b, bph, [&](int buf) {
+                                         (t / tiles_m) * BN + half * S::HALF, b, bph, corner, [&](int buf) {
                                              if (lane == 0) tc::mbar_arrive(aempty0 + 8u * buf);
                                          });
         }
@@ -612,16 +631,22 @@ extern "C" int fp4q_f8_gemm(const uint8_t* codes_a, const float* scales_a, int64
     p.f32 = out_dtype == FP4Q_OUT_F32;
     p.fault = device_fault_word();
     if (!p.fault) return FP4Q_ERR_CUDA;
-    // Few rows of A, or few tiles: rows of A in tiles of 16 to 64, k split over clusters.
+    // Which kernel, by the times measured on 12 shapes (n 3584 to 13824, k 5120 and 18944, m 100 to 1024): a tile of
+    // 128 x 256 takes 0.59 us a block of k, one of 128 x 128 0.32, both after 3 us; a CTA of the few-token kernel 0.38
+    // after 10.  Up to 64 rows B's bytes bound the product and the few-token kernel, with all SMs, always leads
+    // (37 x 3584 x 18944: 21 against 67 us); at 200 x 5120 x 5120 it takes 26 us, tiles of 128 x 128 take 16.
+    const int64_t tiles_m = (m + 127) / 128;
+    const int64_t waves128 = (tiles_m * ((n + 127) / 128) + 147) / 148, waves256 = (tiles_m * ((n + 255) / 256) + 147) / 148;
+    const int64_t ns128 = 3000 + 320 * p.kb * waves128, ns256 = 3000 + 590 * p.kb * waves256;
     const int ntok = m <= 16 ? 16 : m <= 32 ? 32 : 64;
+    const int max_kb = ntok == 16 ? f8gemm::Small<16>::MAX_KB : ntok == 32 ? f8gemm::Small<32>::MAX_KB : f8gemm::Small<64>::MAX_KB;
     const int64_t tiles = ((m + ntok - 1) / ntok) * ((n + 127) / 128);
-    if (m <= 64 || tiles <= 2 * 148) {
-        const int max_kb = ntok == 16 ? f8gemm::Small<16>::MAX_KB : ntok == 32 ? f8gemm::Small<32>::MAX_KB : f8gemm::Small<64>::MAX_KB;
-        const int split = f8gemm::split_of(tiles, p.kb, max_kb);
-        if (split && ntok == 16) return f8gemm::launch_small<16>(p, codes_a, codes_b, k, split, s);
-        if (split && ntok == 32) return f8gemm::launch_small<32>(p, codes_a, codes_b, k, split, s);
-        if (split) return f8gemm::launch_small<64>(p, codes_a, codes_b, k, split, s);
+    const int split = f8gemm::split_of(tiles, p.kb, max_kb);
+    if (split && (m <= 64 || (tiles * split <= 2 * 148 && 10000 + 380 * ((p.kb + split - 1) / split) < (ns128 < ns256 ? ns128 : ns256)))) {
+        if (ntok == 16) return f8gemm::launch_small<16>(p, codes_a, codes_b, k, split, s);
+        if (ntok == 32) return f8gemm::launch_small<32>(p, codes_a, codes_b, k, split, s);
+        return f8gemm::launch_small<64>(p, codes_a, codes_b, k, split, s);
     }
-    if (n > 128 && ((m + 127) / 128) * ((n + 255) / 256) >= 148) return f8gemm::launch<256>(p, codes_b, k, s);
+    if (ns256 <= ns128) return f8gemm::launch<256>(p, codes_b, k, s);
     return f8gemm::launch<128>(p, codes_b, k, s);
 }
