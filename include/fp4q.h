@@ -434,9 +434,9 @@ FP4Q_API int fp4q_gemm(const uint8_t* codes_a, const uint8_t* scales_a, const fl
 FP4Q_API size_t fp4q_mma_scales_size(int64_t rows, int64_t cols, int block);
 
 /*
- * fp4q_f8_quantize -- 8-bit operands beside the 4-bit ones ("Diagnosing FP4
- * inference", Methodology, keeps sensitive layers above 4 bits): E4M3 codes
- * with one fp32 scale per 128 values.
+ * fp4q_f8_quantize -- 8-bit operands beside the 4-bit ones, for layers that do
+ * not bear 4 bits: E4M3 codes with one fp32 scale per 128 values.  The pages
+ * have no counterpart.
  *  x       bf16 [rows][cols] (device, 32-byte aligned); cols a multiple of 16
  *          (FP4Q_ERR_SHAPE otherwise), rows any.  The last group of a row, and
  *          the last tile row, may be short.

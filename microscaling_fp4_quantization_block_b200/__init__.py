@@ -697,6 +697,7 @@ def fp4q_moe(x: torch.Tensor, router: Optional[torch.Tensor], top_k: int, up, do
     callers that call often."""
     if x.dtype != torch.bfloat16 or x.dim() != 2:
         raise ValueError("x must be a 2-D bf16 tensor")
+    fmt = fmt.lower() if isinstance(fmt, str) else fmt
     if fmt not in _MOE_FMT:
         raise ValueError(f"fmt must be one of {sorted(_MOE_FMT)}")
     if _elsewhere(x, stream):

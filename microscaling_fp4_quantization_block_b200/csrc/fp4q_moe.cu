@@ -22,17 +22,28 @@
 //   warps 20-23 add the eight slices of k and finish the item (silu, h; or the
 //     pairs' results) while the next one is multiplied.
 // The weights are widened to fp16 in registers on their way from shared memory
-// into the product; tcgen05.mma, whose operands lie in shared or tensor
-// memory, would need them written back first, and with a few columns per
-// expert the products are far below even the older instruction's rate.
+// into the product; tcgen05.mma, whose operands lie in shared or tensor memory,
+// would need them written back first: 2 bytes a weight through shared memory,
+// four times what the codes cost it.  mma.sync reaches 690 multiply-adds a clock
+// and SM here, 15 columns' worth at the rate HBM delivers FP4 weights, so groups
+// of more than 8 pairs are near its bound.
+//
+// Measured (graph replays; the experts' bytes at the copy rate of 6.55 TB/s in
+// brackets): 1 token, 8 of 64 NVFP4 experts of 2048 x 1024, 29 us (4.4): launch,
+// router, choices and the three waits take 17 of them; 5 tokens over E4M3 experts
+// 59 us (26); 64 tokens over 128 MXFP4 experts of 2048 x 768 176 us (48); over 64
+// NVFP4 experts of 5120 x 1792 319 us (152).  What bounds the long calls is the
+// product warps' work per stage (about 1 us of latencies for 16 KB of codes) and
+// the warps that fill the stages; with the products left out the last takes 245.
 //
 // Activations enter the products as fp16 under one power of two per row (the
 // row's largest value in [2^7, 2^8)): bf16 inputs keep every bit down to 2^-24
 // of the largest and are off by at most 2^-32 of it below that.  h is rounded to
 // fp16 under a power of its own per 32 values, which keeps 11 significant bits
 // where bf16 would keep 8, and brought to its row's power: exact down to 2^-21
-// of the row's largest value, off by at most 2^-24 of it below.  Codes are exact in fp16, and so are NVFP4's products code x
-// UE4M3 scale; E8M0 and fp32 scales multiply the fp32 sums of their blocks.
+// of the row's largest value, off by at most 2^-24 of it below.  Codes are exact
+// in fp16, and so are NVFP4's products code x UE4M3 scale; E8M0 and fp32 scales
+// multiply the fp32 sums of their blocks.
 //
 // Sums across k are in a fixed order and a token's pairs are added in slot
 // order, so results do not depend on timing.  The points where all CTAs
@@ -519,7 +530,7 @@ struct Slots {
     }
 };
 
-// One lane.
+// The weights, by one lane.
 template <int FMT>
 __device__ __forceinline__ void stream_weights(const Params& p, const Shared& sh, uint32_t ring)
 {
@@ -761,7 +772,7 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         const int row = 16 * half + 8 * r + rho;
-                        const uint32_t lead = (uint32_t)((row0 + i * f.second + row) * srb + k0 / 32) & 15u;
+                        const uint32_t lead = ((uint32_t)(row0 + i * f.second + row) * (uint32_t)srb + (uint32_t)(k0 / 32)) & 15u;
                         const uint32_t at = aux + (uint32_t)((32 * i + row) * F::SCALE_PITCH) + lead + 4u * qi;
                         // four bytes that may straddle two words (one block may follow the last: not used)
                         const uint32_t lo = lds32(at & ~3u), hi = lds32((at & ~3u) + 4u * ((at & 3u) != 0u));
@@ -829,7 +840,7 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
                             const int row = 16 * half + 8 * r + rho;
-                            const uint32_t lead = (uint32_t)((row0 + i * f.second + row) * srb + k0 / 16) & 15u;
+                            const uint32_t lead = ((uint32_t)(row0 + i * f.second + row) * (uint32_t)srb + (uint32_t)(k0 / 16)) & 15u;
                             two[i][r] = lds16(aux + (uint32_t)((32 * i + row) * F::SCALE_PITCH) + lead + 2u * (4 * qi + t));
                         }
                 }

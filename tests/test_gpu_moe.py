@@ -292,6 +292,42 @@ def test_workspace_graphs_streams_and_outputs(fq):
     assert fq.fp4q_device_fault() == 0
 
 
+def test_two_host_threads_on_two_streams(fq):
+    """Layers, products for few and for many tokens, in turn on two streams of different
+    priority, from two host threads at once, a workspace each."""
+    import threading
+
+    tokens, experts, top_k, hidden, inter = 24, 16, 4, 1024, 512
+    up = experts_of(fq, "nvfp4", experts, 2 * inter, hidden, hidden ** -0.5, 1)
+    down = experts_of(fq, "nvfp4", experts, hidden, inter, inter ** -0.5, 2)
+    router = workloads.gaussian_bf16(experts, hidden, 0.05, 3, device="cuda")
+    xs = [workloads.gaussian_bf16(tokens, hidden, 1.0, 4 + i, device="cuda") for i in range(2)]
+    a, sa = fq.fp4q_f8_quantize(workloads.gaussian_bf16(700, 2048, 1.0, 9, device="cuda"))
+    b, sb = fq.fp4q_f8_quantize(workloads.gaussian_bf16(4096, 2048, 0.02, 10, device="cuda"), "tile")
+    layer = lambda i, ws, s: fq.fp4q_moe(xs[i], router, top_k, up, down, "nvfp4", workspace=ws, stream=s)[0]
+    calls = [layer, lambda i, ws, s: fq.fp4q_f8_gemm(a, sa, b, sb, stream=s),
+             lambda i, ws, s: fq.fp4q_f8_gemm(a[:5], sa[:5], b, sb, stream=s)]
+    want = [[c(i, None, None).clone() for c in calls] for i in range(2)]
+    torch.cuda.synchronize()
+    wrong = [0, 0]
+
+    def run(i):
+        stream = torch.cuda.Stream(priority=-i)
+        with torch.cuda.stream(stream):
+            ws = torch.zeros((8 << 20,), dtype=torch.uint8, device="cuda")
+        for n in range(60):
+            y = calls[(n + i) % 3](i, ws, stream)
+            with torch.cuda.stream(stream):
+                wrong[i] += int(not torch.equal(y, want[i][(n + i) % 3]))
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert wrong == [0, 0] and fq.fp4q_device_fault() == 0
+
+
 def test_run_of_the_operators_together(fq):
     """A decoder layer's linear part as it would be used: activations quantized to 8 bits and
     multiplied, the result through the experts, and the experts' result multiplied again."""
