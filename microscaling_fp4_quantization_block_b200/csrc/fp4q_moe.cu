@@ -649,6 +649,23 @@ __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, u
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same onto zeros.
+__device__ __forceinline__ void mma16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                           uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// 2^(byte - 127) of byte b of four, as e8m0_decode but for 255, which is infinity here.
+template <int B>
+__device__ __forceinline__ float e8m0_byte(uint32_t four)
+{
+    const uint32_t at23 = B == 3 ? four >> 1 : four << (23 - 8 * B);
+    return as_f32(max(at23 & 0x7f800000u, 0x00400000u));
+}
+
 // Eight E2M1 codes -> four f16 pairs, in order.
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t (&h)[4])
 {
@@ -705,6 +722,11 @@ __device__ __forceinline__ uint32_t lds16(uint32_t a)
 }
 
 __device__ __forceinline__ void sums_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * SUM_WARPS) : "memory"); }
+
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
 
 // A place in the CTA's sequence of stages.
 struct Cursor {
@@ -790,9 +812,9 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
                     }
                 }
                 // block by block: with all blocks' loads ahead of the products it took 10 % longer (registers)
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    if (b >= left) break;
+                const uint32_t wq = w0 + ((uint32_t)(c16 ^ (rho & 4)) << 4) + 4u * t;
+                auto block = [&](auto which_block) {
+                    constexpr int b = decltype(which_block)::value;
                     uint4 bf[NT];
 #pragma unroll
                     for (int c = 0; c < NT; ++c) {
@@ -805,25 +827,27 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
                             bf[c].z = mul_f16x2(bf[c].z, m), bf[c].w = mul_f16x2(bf[c].w, m);
                         }
                     }
+                    const uint32_t wb = wq + ((uint32_t)(b ^ (rho & 3)) << 4);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const uint32_t wa = w0 + (uint32_t)(i * BOX_BYTES) + ((uint32_t)((c16 + b) ^ rho) << 4) + 4u * t;
                         uint32_t a0[4], a1[4];
-                        widen4(lds32(wa), a0);
-                        widen4(lds32(wa + 1024u), a1);
-                        const float s0 = e8m0_decode((sc[i][0] >> (8 * b)) & 255u);
-                        const float s1 = e8m0_decode((sc[i][1] >> (8 * b)) & 255u);
+                        widen4(lds32(wb + (uint32_t)(i * BOX_BYTES)), a0);
+                        widen4(lds32(wb + (uint32_t)(i * BOX_BYTES + 1024)), a1);
+                        const float s0 = e8m0_byte<b>(sc[i][0]), s1 = e8m0_byte<b>(sc[i][1]);
 #pragma unroll
                         for (int c = 0; c < NT; ++c) {
-                            float d[4] = {};
-                            mma16(d, a0[0], a1[0], a0[1], a1[1], bf[c].x, bf[c].y);
+                            float d[4];
+                            mma16_zero(d, a0[0], a1[0], a0[1], a1[1], bf[c].x, bf[c].y);
                             mma16(d, a0[2], a1[2], a0[3], a1[3], bf[c].z, bf[c].w);
-                            float(&o)[4] = acc[i][c];
-                            upk(fma2(pk(d[0], d[1]), pk(s0, s0), pk(o[0], o[1])), o[0], o[1]);
-                            upk(fma2(pk(d[2], d[3]), pk(s1, s1), pk(o[2], o[3])), o[2], o[3]);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) acc[i][c][j] = __fmaf_rn(d[j], j < 2 ? s0 : s1, acc[i][c][j]);
                         }
                     }
-                }
+                };
+                block(Int<0>{});
+                if (left > 1) block(Int<1>{});
+                if (left > 2) block(Int<2>{});
+                if (left > 3) block(Int<3>{});
             } else {
                 constexpr int PIECES = FMT == kNv ? 4 : 2;   // 16-byte pieces of activations per lane
                 uint4 bf[NT][PIECES], w[2][2];               // all loads first
@@ -889,7 +913,7 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
                             }
                         }
                     } else {
-                        float d[NT][4] = {};
+                        float d[NT][4];
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             uint32_t a0[4], a1[4];
@@ -897,7 +921,10 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
                             widen8(u1[2 * j], u1[2 * j + 1], a1);
 #pragma unroll
                             for (int c = 0; c < NT; ++c) {
-                                mma16(d[c], a0[0], a1[0], a0[1], a1[1], bf[c][j].x, bf[c][j].y);
+                                if (j == 0)
+                                    mma16_zero(d[c], a0[0], a1[0], a0[1], a1[1], bf[c][j].x, bf[c][j].y);
+                                else
+                                    mma16(d[c], a0[0], a1[0], a0[1], a1[1], bf[c][j].x, bf[c][j].y);
                                 mma16(d[c], a0[2], a1[2], a0[3], a1[3], bf[c][j].z, bf[c][j].w);
                             }
                         }
