@@ -123,7 +123,7 @@ struct Params {
 struct Plan {                       // what the CTA knows once the choices are made
     int groups;                     // (expert, up to GROUP pairs)
     int widest;                     // pairs of the largest group
-    int pitch, buffers;             // of the partial sums: floats per row, and how many
+    int buffers;                    // of partial sums: two where no item has more than 8 columns
     int stages;                     // an even number: a slot of the ring belongs to one set of product warps and one aux warp
     uint32_t aux_bytes, acts_at, inverse_at;    // what a stage holds beside its weights: scale bytes, records, 1 / the rows' powers
 };
@@ -438,7 +438,6 @@ __device__ void make_plan(const Params& p, Shared& sh)
             Plan& q = sh.plan;
             q.groups = groups;
             q.widest = widest;
-            q.pitch = widest > 8 ? 17 : 9;
             q.buffers = widest > 8 ? 1 : 2;
             q.acts_at = TILE * F::SCALE_PITCH;
             q.inverse_at = q.acts_at + widest * F::RECORD;
@@ -479,6 +478,24 @@ struct Phase {
     int rows;                       // rows per expert
     int second;                     // rows from an item's first box to its second
     int step;                       // rows from one item to the next
+    int hop_groups, hop_tiles;      // gridDim.x items on: so many groups and tiles
+};
+
+// This CTA's items of a phase, one after the other.
+struct Item {
+    int left;                       // items of this CTA, this one included
+    int group, tile;
+
+    __device__ __forceinline__ explicit Item(const Phase& f)
+        : left(f.first < f.items ? (f.items - f.first + (int)gridDim.x - 1) / (int)gridDim.x : 0),
+          group(f.first / f.tiles), tile(f.first % f.tiles) {}
+    __device__ __forceinline__ void next(const Phase& f)
+    {
+        --left;
+        group += f.hop_groups;
+        tile += f.hop_tiles;
+        if (tile >= f.tiles) tile -= f.tiles, ++group;
+    }
 };
 
 __device__ __forceinline__ Phase phase_of(const Params& p, const Plan& q, int which)
@@ -505,6 +522,8 @@ __device__ __forceinline__ Phase phase_of(const Params& p, const Plan& q, int wh
         f.second = 32;
         f.step = TILE;
     }
+    f.hop_groups = (int)gridDim.x / f.tiles;
+    f.hop_tiles = (int)gridDim.x % f.tiles;
     return f;
 }
 
@@ -539,9 +558,8 @@ __device__ __forceinline__ void stream_weights(const Params& p, const Shared& sh
     for (int which = 0; which < 2; ++which) {
         const Phase f = phase_of(p, sh.plan, which);
         const int row_bytes = F::f8 ? f.k : f.k / 2;
-        for (int it = f.first; it < f.items; it += gridDim.x) {
-            const int g = it / f.tiles, tile = it - g * f.tiles;
-            const int row0 = sh.g_expert[g] * f.rows + tile * f.step;      // experts * rows is below 2^31
+        for (Item it(f); it.left > 0; it.next(f)) {
+            const int row0 = sh.g_expert[it.group] * f.rows + it.tile * f.step;      // experts * rows is below 2^31
             for (int b0 = 0; b0 < row_bytes; b0 += F::CHUNKS * 128) {
                 if (!s.wait_empty(p.fault)) return;
                 const uint32_t st = ring + (uint32_t)(s.at * WEIGHT_BYTES), bar = s.full0 + 8u * s.at;
@@ -578,8 +596,8 @@ __device__ __forceinline__ void stream_aux(const Params& p, const Shared& sh, ui
         const Phase f = phase_of(p, sh.plan, which);
         const int srb = f.k / (FMT == kNv ? 16 : 32), stages = which == 0 ? p.xstages : p.hstages;
         bool ready = which == 0;
-        for (int it = f.first; it < f.items; it += gridDim.x) {
-            const int g = it / f.tiles, tile = it - g * f.tiles, n = sh.g_count[g];
+        for (Item it(f); it.left > 0; it.next(f)) {
+            const int g = it.group, tile = it.tile, n = sh.g_count[g];
             const int row0 = sh.g_expert[g] * f.rows + tile * f.step;
             // this lane's rows: lane of each box; where their bytes begin, rounded down, and by how much
             const uint8_t* src[2];
@@ -758,6 +776,18 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
         f8_scales = static_cast<const float*>(f.m->scales) + (int64_t)(row0 >> 7) * (f.k >> 7);
         f8_second = ((row0 + f.second) >> 7) * (f.k >> 7) - (row0 >> 7) * (f.k >> 7);
     }
+    // where the scale bytes of this lane's rows lie: a stage's copies begin at a multiple of 16 bytes of each row's
+    // place in memory, so what precedes the bytes asked for is the same all through the item
+    uint32_t scale_at[2][2] = {};
+    if constexpr (FMT != kF8) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint32_t row = (uint32_t)(16 * half + 8 * r + rho);
+                scale_at[i][r] = (32u * i + row) * F::SCALE_PITCH + (((uint32_t)(row0 + i * f.second) + row) * (uint32_t)srb & 15u);
+            }
+    }
     int col[NT];                                             // columns past the last pair repeat it
 #pragma unroll
     for (int c = 0; c < NT; ++c) col[c] = min(8 * c + g, n - 1);
@@ -793,9 +823,7 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const int row = 16 * half + 8 * r + rho;
-                        const uint32_t lead = ((uint32_t)(row0 + i * f.second + row) * (uint32_t)srb + (uint32_t)(k0 / 32)) & 15u;
-                        const uint32_t at = aux + (uint32_t)((32 * i + row) * F::SCALE_PITCH) + lead + 4u * qi;
+                        const uint32_t at = aux + scale_at[i][r] + 4u * qi;
                         // four bytes that may straddle two words (one block may follow the last: not used)
                         const uint32_t lo = lds32(at & ~3u), hi = lds32((at & ~3u) + 4u * ((at & 3u) != 0u));
                         sc[i][r] = __funnelshift_r(lo, hi, 8u * (at & 3u));
@@ -862,11 +890,7 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const int row = 16 * half + 8 * r + rho;
-                            const uint32_t lead = ((uint32_t)(row0 + i * f.second + row) * (uint32_t)srb + (uint32_t)(k0 / 16)) & 15u;
-                            two[i][r] = lds16(aux + (uint32_t)((32 * i + row) * F::SCALE_PITCH) + lead + 2u * (4 * qi + t));
-                        }
+                        for (int r = 0; r < 2; ++r) two[i][r] = lds16(aux + scale_at[i][r] + 2u * (4 * qi + t));
                 }
 #pragma unroll
                 for (int c = 0; c < NT; ++c) {
@@ -960,16 +984,17 @@ __device__ __forceinline__ void item_products(const Params& p, const Shared& sh,
     float acc[2][NT][4] = {};
     item<FMT, NT, WHICH>(p, sh.plan, ring, f, row0, n, cur, acc);
 
-    const int g = lane >> 2, t = lane & 3, half = (warp >> 2) & 1, pitch = sh.plan.pitch;
+    const int g = lane >> 2, t = lane & 3, half = (warp >> 2) & 1;
+    constexpr int PITCH = 8 * NT + 1;                        // floats per row of the partial sums
     const int slice = (warp >> 3) * 4 + (warp & 3), rho = (g >> 1) | ((g & 1) << 2);
     if (cur.live) cur.live = __all_sync(0xffffffffu, tc::wait_phase(smem_of(&sh.summed[buf.at]), buf.phase ^ 1u, p.fault));
-    float* to = red + (buf.at * SLICES * TILE + slice * TILE + 16 * half + rho) * pitch + 2 * t;
+    float* to = red + (buf.at * SLICES * TILE + slice * TILE + 16 * half + rho) * PITCH + 2 * t;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int c = 0; c < NT; ++c)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) to[(32 * i + 8 * (j >> 1)) * pitch + 8 * c + (j & 1)] = acc[i][c][j];
+            for (int j = 0; j < 4; ++j) to[(32 * i + 8 * (j >> 1)) * PITCH + 8 * c + (j & 1)] = acc[i][c][j];
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(smem_of(&sh.summable[buf.at]));
     buf.next();
@@ -979,9 +1004,8 @@ template <int FMT, int WHICH>
 __device__ __forceinline__ void multiply(const Params& p, const Shared& sh, uint32_t ring, float* red, Cursor& cur, Buffers& buf)
 {
     const Phase f = phase_of(p, sh.plan, WHICH);
-    for (int it = f.first; it < f.items; it += gridDim.x) {
-        const int grp = it / f.tiles, n = sh.g_count[grp];
-        const int row0 = sh.g_expert[grp] * f.rows + (it - grp * f.tiles) * f.step;
+    for (Item it(f); it.left > 0; it.next(f)) {
+        const int n = sh.g_count[it.group], row0 = sh.g_expert[it.group] * f.rows + it.tile * f.step;
         if (n > 8)
             item_products<FMT, 2, WHICH>(p, sh, ring, red, f, row0, n, cur, buf);
         else
@@ -996,9 +1020,9 @@ __device__ __forceinline__ void add_slices(const Params& p, const Shared& sh, co
 {
     using F = Format<FMT>;
     const Phase f = phase_of(p, sh.plan, WHICH);
-    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - (CONSUMERS + 1 + AUX_WARPS + SPARE_WARPS), pitch = sh.plan.pitch;
-    for (int it = f.first; it < f.items; it += gridDim.x, buf.next()) {
-        const int grp = it / f.tiles, tile = it - grp * f.tiles, e = sh.g_expert[grp], n = sh.g_count[grp];
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - (CONSUMERS + 1 + AUX_WARPS + SPARE_WARPS);
+    for (Item it(f); it.left > 0; it.next(f), buf.next()) {
+        const int grp = it.group, tile = it.tile, e = sh.g_expert[grp], n = sh.g_count[grp];
         const uint16_t* list = sh.list + sh.g_first[grp];
         const float gs = FMT == kNv && f.m->gscale ? __ldg(f.m->gscale + e * f.m->gstride) : 1.0f;
         float pow = 0.0f, inv;                               // lane c: of column c
@@ -1009,6 +1033,7 @@ __device__ __forceinline__ void add_slices(const Params& p, const Shared& sh, co
                 power_of(__ldcg(p.hmax + list[lane]), pow, inv);
         }
         if (live) live = __all_sync(0xffffffffu, tc::wait_phase(smem_of(&sh.summable[buf.at]), buf.phase, p.fault));
+        const int pitch = n > 8 ? 17 : 9;
         const float* from = red + (buf.at * SLICES * TILE + lane) * pitch;
         // a warp per pair, a lane for rows l and l + 32
         for (int c = warp; c < n; c += SUM_WARPS) {
