@@ -1118,6 +1118,8 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(const __grid_constant__
             tc::mbar_init(smem_of(&sh.summed[i]), (uint32_t)SUM_WARPS);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.up.map)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.down.map)) : "memory");
     }
     convert_x<FMT>(p, reinterpret_cast<unsigned int*>(red));
     if (p.router) route_logits(p);
