@@ -8,19 +8,19 @@
 // each read once, so everything else is arranged around one stream of them:
 // one CTA per SM walks a static share of (group, 64-row tile) items, a group
 // being up to 16 pairs of one expert, first of the gate/up matrices (32 rows
-// of each), then of the down matrices.  Per CTA
-//   warp 16 streams the items' weight rows through a ring of shared-memory
-//     stages (TMA tiles of 32 rows x 128 bytes, 128-byte swizzle).  It runs ahead
-//     of the layer's dependencies: the first down tiles are on their way while h
-//     is still being computed;
-//   warps 17 and 18 take turns to add the rows' scale bytes and the pairs'
-//     activations (16-byte cp.async: as bulk copies of 32 bytes the scale bytes
-//     took 45 ns each, one after the other, eight times the weights' time);
-//   warps 0-15 multiply: two sets take turns at the stages, in a set 4 quarters
-//     of the stage's k by 2 halves of its rows, mma.sync m16n8k16 with the
-//     weights as the 16 rows and the pairs as the 8 columns;
-//   warps 20-23 add the eight slices of k and finish the item (silu, h; or the
-//     pairs' results) while the next one is multiplied.
+// of each), then of the down matrices, two items at a time.  Each of the two
+// streams has half of a ring of shared-memory stages and, of the CTA's warps,
+//   one (16, 18) that fetches the items' weight rows (TMA tiles of 32 rows x 128
+//     bytes, 128-byte swizzle), ahead of the layer's dependencies: the first
+//     down tiles are on their way while h is still being computed;
+//   one (17, 19) that adds the rows' scale bytes and the pairs' activations
+//     (16-byte cp.async: as bulk copies of 32 bytes the scale bytes took 45 ns
+//     each, one after the other, eight times the weights' time);
+//   eight (0-7, 8-15) that multiply, 4 quarters of a stage's k by 2 halves of its
+//     rows, mma.sync m16n8k16 with the weights as the 16 rows and the pairs as
+//     the 8 columns;
+//   two (20 and 21, 22 and 23) that add the four slices of k and finish the item
+//     (silu, h; or the pairs' results) while the next one is multiplied.
 // The weights are widened to fp16 in registers on their way from shared memory
 // into the product; tcgen05.mma, whose operands lie in shared or tensor memory,
 // would need them written back first: 2 bytes a weight through shared memory,
@@ -68,19 +68,20 @@ namespace moe {
 
 constexpr int MAX_TOKENS = FP4Q_MOE_MAX_TOKENS, MAX_TOPK = FP4Q_MOE_MAX_TOPK, MAX_EXPERTS = FP4Q_MOE_MAX_EXPERTS;
 constexpr int MAX_PAIRS = MAX_TOKENS * MAX_TOPK;
-constexpr int CONSUMERS = 16;                           // warps that multiply, two sets of 8
-constexpr int AUX_WARPS = 2;                            // that copy scale bytes and activations
-constexpr int SPARE_WARPS = 1;                          // so that each warpgroup has registers of its own
-constexpr int SUM_WARPS = 4;                            // that add an item's slices and write its results
-constexpr int THREADS = 32 * (CONSUMERS + 1 + AUX_WARPS + SPARE_WARPS + SUM_WARPS);
+constexpr int STREAMS = 2;                              // items in work at the same time
+constexpr int SET = 8;                                  // warps that multiply, per stream
+constexpr int CONSUMERS = STREAMS * SET;
+constexpr int SUM_WARPS = 2;                            // per stream: add an item's slices and write its results
+constexpr int FIRST_COPY = CONSUMERS, FIRST_SUM = FIRST_COPY + 2 * STREAMS;    // per stream a warp for weights, one for the rest
+constexpr int THREADS = 32 * (FIRST_SUM + STREAMS * SUM_WARPS);
 constexpr int REGS_PRODUCTS = 96, REGS_OTHERS = 48;     // 512 x 96 + 256 x 48 = 768 x 80, the launch's registers
 constexpr int GROUP = 16;                               // pairs per group, at most
 constexpr int TILE = 64;                                // rows per item: two boxes of 32
 constexpr int BOX_BYTES = 32 * 128;
 constexpr int WEIGHT_BYTES = 2 * 2 * BOX_BYTES;         // per stage: two 128-byte chunks of two boxes
-constexpr int SLICES = CONSUMERS / 2;                   // of k, per item
+constexpr int SLICES = 4;                               // of k, per item
 constexpr int RING_BYTES = 172 * 1024;
-constexpr int RED_BYTES = 36 * 1024;                    // partial sums: two buffers of 8 columns or one of 16
+constexpr int RED_BYTES = 36 * 1024;                    // partial sums: per stream two buffers of 8 columns or one of 16
 constexpr int SMEM_BYTES = 1024 + RING_BYTES + RED_BYTES;
 constexpr int MAX_STAGES = 12;
 constexpr int MIN_STAGES = 4;
@@ -123,8 +124,8 @@ struct Params {
 struct Plan {                       // what the CTA knows once the choices are made
     int groups;                     // (expert, up to GROUP pairs)
     int widest;                     // pairs of the largest group
-    int buffers;                    // of partial sums: two where no item has more than 8 columns
-    int stages;                     // an even number: a slot of the ring belongs to one set of product warps and one aux warp
+    int buffers;                    // of partial sums per stream: two where no item has more than 8 columns
+    int stages;                     // an even number: every other slot of the ring is a stream's
     uint32_t aux_bytes, acts_at, inverse_at;    // what a stage holds beside its weights: scale bytes, records, 1 / the rows' powers
 };
 
@@ -137,10 +138,9 @@ struct Shared {
     uint16_t g_expert[MAX_PAIRS], g_first[MAX_PAIRS];
     uint8_t g_count[MAX_PAIRS];
     uint64_t full[MAX_STAGES], empty[MAX_STAGES];
-    uint64_t summed[2], summable[2];            // a buffer of partial sums: free, complete
+    uint64_t summed[STREAMS][2], summable[STREAMS][2];      // a buffer of partial sums: free, complete
     Plan plan;
 };
-static_assert(AUX_WARPS == 2 && MIN_STAGES > AUX_WARPS, "the ring is even");
 static_assert(sizeof(Shared) + SMEM_BYTES + 1024 <= 227 * 1024, "shared memory per CTA");
 
 // ---------------------------------------------------------------- formats
@@ -478,17 +478,21 @@ struct Phase {
     int rows;                       // rows per expert
     int second;                     // rows from an item's first box to its second
     int step;                       // rows from one item to the next
-    int hop_groups, hop_tiles;      // gridDim.x items on: so many groups and tiles
+    int hop_groups, hop_tiles;      // a stream's next item: so many groups and tiles on
 };
 
-// This CTA's items of a phase, one after the other.
+// A stream's items of a phase, one after the other: every STREAMS-th of the CTA's.
 struct Item {
-    int left;                       // items of this CTA, this one included
+    int left;                       // items, this one included
     int group, tile;
 
-    __device__ __forceinline__ explicit Item(const Phase& f)
-        : left(f.first < f.items ? (f.items - f.first + (int)gridDim.x - 1) / (int)gridDim.x : 0),
-          group(f.first / f.tiles), tile(f.first % f.tiles) {}
+    __device__ __forceinline__ Item(const Phase& f, int stream)
+    {
+        const int first = f.first + stream * (int)gridDim.x, hop = STREAMS * (int)gridDim.x;
+        left = first < f.items ? (f.items - first + hop - 1) / hop : 0;
+        group = first / f.tiles;
+        tile = first - group * f.tiles;
+    }
     __device__ __forceinline__ void next(const Phase& f)
     {
         --left;
@@ -522,43 +526,43 @@ __device__ __forceinline__ Phase phase_of(const Params& p, const Plan& q, int wh
         f.second = 32;
         f.step = TILE;
     }
-    f.hop_groups = (int)gridDim.x / f.tiles;
-    f.hop_tiles = (int)gridDim.x % f.tiles;
+    f.hop_groups = STREAMS * (int)gridDim.x / f.tiles;
+    f.hop_tiles = STREAMS * (int)gridDim.x % f.tiles;
     return f;
 }
 
-// A place in the CTA's sequence of stages, `step` stages at a time.  step divides
-// the ring, so that a slot always belongs to the same warp: a barrier's parity
-// tells a phase only from the one before it, so whoever waits for a slot must
-// have seen each of its rounds.
+// A place in a stream's sequence of stages.  The ring is even, so that a slot
+// always belongs to the same stream: a barrier's parity tells a phase only from
+// the one before it, so whoever waits for a slot must have seen each of its
+// rounds.
 struct Slots {
     uint32_t full0, empty0;
-    int n, step, at;
+    int n, at;
     uint32_t phase;
 
-    __device__ Slots(const Shared& sh, int first, int by)
-        : full0(smem_of(sh.full)), empty0(smem_of(sh.empty)), n(sh.plan.stages), step(by), at(first), phase(1u) {}
+    __device__ Slots(const Shared& sh, int stream)
+        : full0(smem_of(sh.full)), empty0(smem_of(sh.empty)), n(sh.plan.stages), at(stream), phase(1u) {}
     __device__ __forceinline__ bool wait_empty(unsigned int* fault) const
     {
         return tc::wait_phase(empty0 + 8u * at, phase, fault);
     }
     __device__ __forceinline__ void next()
     {
-        at += step;
-        if (at >= n) at -= n, phase ^= 1u;                   // step is below n
+        at += STREAMS;
+        if (at >= n) at -= n, phase ^= 1u;
     }
 };
 
 // The weights, by one lane.
 template <int FMT>
-__device__ __forceinline__ void stream_weights(const Params& p, const Shared& sh, uint32_t ring)
+__device__ __forceinline__ void stream_weights(const Params& p, const Shared& sh, uint32_t ring, int stream)
 {
     using F = Format<FMT>;
-    Slots s(sh, 0, 1);
+    Slots s(sh, stream);
     for (int which = 0; which < 2; ++which) {
         const Phase f = phase_of(p, sh.plan, which);
         const int row_bytes = F::f8 ? f.k : f.k / 2;
-        for (Item it(f); it.left > 0; it.next(f)) {
+        for (Item it(f, stream); it.left > 0; it.next(f)) {
             const int row0 = sh.g_expert[it.group] * f.rows + it.tile * f.step;      // experts * rows is below 2^31
             for (int b0 = 0; b0 < row_bytes; b0 += F::CHUNKS * 128) {
                 if (!s.wait_empty(p.fault)) return;
@@ -579,24 +583,23 @@ __device__ __forceinline__ void stream_weights(const Params& p, const Shared& sh
 
 // What a stage holds beside its weights: the rows' scale bytes, widened to
 // 16-byte boundaries (every matrix of scales ends on one), and the pairs'
-// activations.  AUX_WARPS warps take turns at the stages: one warp alone took
-// 0.35 us a stage, as long as HBM needs for its weights.
+// activations.  A warp takes 0.35 us a stage for it, as long as HBM needs for the
+// weights: a warp per stream keeps up.
 template <int FMT>
-__device__ __forceinline__ void stream_aux(const Params& p, const Shared& sh, uint32_t ring, int turn)
+__device__ __forceinline__ void stream_aux(const Params& p, const Shared& sh, uint32_t ring, int stream)
 {
     using F = Format<FMT>;
     constexpr int PIECES = F::SCALE_PITCH / 16;              // of 16 bytes, per row
     const int lane = threadIdx.x & 31;
     const uint32_t aux0 = ring + (uint32_t)sh.plan.stages * WEIGHT_BYTES, aux_bytes = sh.plan.aux_bytes;
     const uint32_t act_at = sh.plan.acts_at + (uint32_t)(lane * F::RECORD), inverse_at = sh.plan.inverse_at + 4u * lane;
-    Slots s(sh, turn, AUX_WARPS);
-    int ahead = turn;                                        // stages before this warp's next one
+    Slots s(sh, stream);
     fence_async();                                           // x was converted by ordinary stores
     for (int which = 0; which < 2; ++which) {
         const Phase f = phase_of(p, sh.plan, which);
         const int srb = f.k / (FMT == kNv ? 16 : 32), stages = which == 0 ? p.xstages : p.hstages;
         bool ready = which == 0;
-        for (Item it(f); it.left > 0; it.next(f)) {
+        for (Item it(f, stream); it.left > 0; it.next(f)) {
             const int g = it.group, tile = it.tile, n = sh.g_count[g];
             const int row0 = sh.g_expert[g] * f.rows + tile * f.step;
             // this lane's rows: lane of each box; where their bytes begin, rounded down, and by how much
@@ -619,8 +622,7 @@ __device__ __forceinline__ void stream_aux(const Params& p, const Shared& sh, ui
             const uint8_t* acts = (which == 0 ? p.xs : p.h) + (int64_t)row * stages * F::RECORD;
             float pow, inv = 0.0f;
             if (ready && which == 1 && lane < n) power_of(__ldcg(p.hmax + row), pow, inv);
-            int i = ahead;
-            for (; i < stages; i += AUX_WARPS) {
+            for (int i = 0; i < stages; ++i) {
                 const bool ok = s.wait_empty(p.fault);
                 if (!__all_sync(0xffffffffu, ok)) return;
                 const uint32_t aux = aux0 + (uint32_t)s.at * aux_bytes, bar = s.full0 + 8u * s.at;
@@ -653,7 +655,6 @@ __device__ __forceinline__ void stream_aux(const Params& p, const Shared& sh, ui
                 if (lane < n) tc::bulk_load(aux + act_at, acts + i * F::RECORD, (uint32_t)F::RECORD, bar);
                 s.next();
             }
-            ahead = i - stages;
         }
     }
 }
@@ -739,18 +740,18 @@ __device__ __forceinline__ uint32_t lds16(uint32_t a)
     return r;
 }
 
-__device__ __forceinline__ void sums_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * SUM_WARPS) : "memory"); }
+__device__ __forceinline__ void sums_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * STREAMS * SUM_WARPS) : "memory"); }
 
 template <int N>
 struct Int {
     static constexpr int value = N;
 };
 
-// A place in the CTA's sequence of stages.
+// A place in a stream's sequence of stages.
 struct Cursor {
     uint32_t full0, empty0;
     int stages, slot;
-    uint32_t phase, seq;
+    uint32_t phase, seq;            // of its stages so far
     bool live;
 };
 
@@ -767,7 +768,6 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
     const uint32_t full0 = cur.full0, empty0 = cur.empty0, aux0 = ring + (uint32_t)cur.stages * WEIGHT_BYTES;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3, half = (warp >> 2) & 1;
-    const uint32_t set = (uint32_t)warp >> 3;
     const int rho = (g >> 1) | ((g & 1) << 2);
     const int srb = FMT == kNv ? f.k / 16 : f.k / 32;
     const float* f8_scales = nullptr;                        // of this item's first box
@@ -795,10 +795,8 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
     for (int k0 = 0; k0 < f.k; k0 += F::VALUES) {
         const int s = cur.slot;
         const uint32_t ph = cur.phase;
-        if (++cur.slot == cur.stages) cur.slot = 0, cur.phase ^= 1u;
-        const uint32_t seq = cur.seq++;
-        if ((seq & 1u) != set) continue;
-        const int qi = (int)(((uint32_t)warp + (seq >> 1)) & 3u);      // turns, so that short stages load all alike
+        if ((cur.slot += STREAMS) >= cur.stages) cur.slot -= cur.stages, cur.phase ^= 1u;
+        const int qi = (int)(((uint32_t)warp + cur.seq++) & 3u);       // turns, so that short stages load all alike
         const int values = min(F::VALUES, f.k - k0);
         float fs[2] = {};
         if (FMT == kF8 && qi * F::QUARTER < values) {
@@ -965,8 +963,10 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
     }
 }
 
-// A place in the CTA's sequence of buffers of partial sums.
+// A place in a stream's sequence of buffers of partial sums.
 struct Buffers {
+    uint32_t summed, summable;      // the stream's barriers
+    float* sums;                    // and its shared memory
     int n, at;
     uint32_t phase;
     __device__ __forceinline__ void next()
@@ -977,8 +977,8 @@ struct Buffers {
 
 // The product warps' part of one phase.
 template <int FMT, int NT, int WHICH>
-__device__ __forceinline__ void item_products(const Params& p, const Shared& sh, uint32_t ring, float* red, const Phase& f,
-                                              int row0, int n, Cursor& cur, Buffers& buf)
+__device__ __forceinline__ void item_products(const Params& p, const Shared& sh, uint32_t ring, const Phase& f, int row0,
+                                              int n, Cursor& cur, Buffers& buf)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float acc[2][NT][4] = {};
@@ -986,9 +986,9 @@ __device__ __forceinline__ void item_products(const Params& p, const Shared& sh,
 
     const int g = lane >> 2, t = lane & 3, half = (warp >> 2) & 1;
     constexpr int PITCH = 8 * NT + 1;                        // floats per row of the partial sums
-    const int slice = (warp >> 3) * 4 + (warp & 3), rho = (g >> 1) | ((g & 1) << 2);
-    if (cur.live) cur.live = __all_sync(0xffffffffu, tc::wait_phase(smem_of(&sh.summed[buf.at]), buf.phase ^ 1u, p.fault));
-    float* to = red + (buf.at * SLICES * TILE + slice * TILE + 16 * half + rho) * PITCH + 2 * t;
+    const int slice = warp & 3, rho = (g >> 1) | ((g & 1) << 2);
+    if (cur.live) cur.live = __all_sync(0xffffffffu, tc::wait_phase(buf.summed + 8u * buf.at, buf.phase ^ 1u, p.fault));
+    float* to = buf.sums + (buf.at * SLICES * TILE + slice * TILE + 16 * half + rho) * PITCH + 2 * t;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -996,32 +996,32 @@ __device__ __forceinline__ void item_products(const Params& p, const Shared& sh,
 #pragma unroll
             for (int j = 0; j < 4; ++j) to[(32 * i + 8 * (j >> 1)) * PITCH + 8 * c + (j & 1)] = acc[i][c][j];
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive(smem_of(&sh.summable[buf.at]));
+    if (lane == 0) tc::mbar_arrive(buf.summable + 8u * buf.at);
     buf.next();
 }
 
 template <int FMT, int WHICH>
-__device__ __forceinline__ void multiply(const Params& p, const Shared& sh, uint32_t ring, float* red, Cursor& cur, Buffers& buf)
+__device__ __forceinline__ void multiply(const Params& p, const Shared& sh, uint32_t ring, int stream, Cursor& cur, Buffers& buf)
 {
     const Phase f = phase_of(p, sh.plan, WHICH);
-    for (Item it(f); it.left > 0; it.next(f)) {
+    for (Item it(f, stream); it.left > 0; it.next(f)) {
         const int n = sh.g_count[it.group], row0 = sh.g_expert[it.group] * f.rows + it.tile * f.step;
         if (n > 8)
-            item_products<FMT, 2, WHICH>(p, sh, ring, red, f, row0, n, cur, buf);
+            item_products<FMT, 2, WHICH>(p, sh, ring, f, row0, n, cur, buf);
         else
-            item_products<FMT, 1, WHICH>(p, sh, ring, red, f, row0, n, cur, buf);
+            item_products<FMT, 1, WHICH>(p, sh, ring, f, row0, n, cur, buf);
     }
 }
 
-// The summing warps' part: the eight slices of k, in order, to h (WHICH 0) or
+// The summing warps' part: the four slices of k, in order, to h (WHICH 0) or
 // to the pairs' results (1), beside the next item's products.
 template <int FMT, int WHICH>
-__device__ __forceinline__ void add_slices(const Params& p, const Shared& sh, const float* red, Buffers& buf, bool& live)
+__device__ __forceinline__ void add_slices(const Params& p, const Shared& sh, int stream, Buffers& buf, bool& live)
 {
     using F = Format<FMT>;
     const Phase f = phase_of(p, sh.plan, WHICH);
-    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - (CONSUMERS + 1 + AUX_WARPS + SPARE_WARPS);
-    for (Item it(f); it.left > 0; it.next(f), buf.next()) {
+    const int lane = threadIdx.x & 31, warp = ((threadIdx.x >> 5) - FIRST_SUM) % SUM_WARPS;
+    for (Item it(f, stream); it.left > 0; it.next(f), buf.next()) {
         const int grp = it.group, tile = it.tile, e = sh.g_expert[grp], n = sh.g_count[grp];
         const uint16_t* list = sh.list + sh.g_first[grp];
         const float gs = FMT == kNv && f.m->gscale ? __ldg(f.m->gscale + e * f.m->gstride) : 1.0f;
@@ -1032,9 +1032,9 @@ __device__ __forceinline__ void add_slices(const Params& p, const Shared& sh, co
             else
                 power_of(__ldcg(p.hmax + list[lane]), pow, inv);
         }
-        if (live) live = __all_sync(0xffffffffu, tc::wait_phase(smem_of(&sh.summable[buf.at]), buf.phase, p.fault));
+        if (live) live = __all_sync(0xffffffffu, tc::wait_phase(buf.summable + 8u * buf.at, buf.phase, p.fault));
         const int pitch = n > 8 ? 17 : 9;
-        const float* from = red + (buf.at * SLICES * TILE + lane) * pitch;
+        const float* from = buf.sums + (buf.at * SLICES * TILE + lane) * pitch;
         // a warp per pair, a lane for rows l and l + 32
         for (int c = warp; c < n; c += SUM_WARPS) {
             float a = 0.0f, b = 0.0f;
@@ -1072,7 +1072,7 @@ __device__ __forceinline__ void add_slices(const Params& p, const Shared& sh, co
             }
         }
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(smem_of(&sh.summed[buf.at]));
+        if (lane == 0) tc::mbar_arrive(buf.summed + 8u * buf.at);
     }
 }
 
@@ -1080,7 +1080,7 @@ __device__ __forceinline__ void add_slices(const Params& p, const Shared& sh, co
 __device__ __forceinline__ void sums_count(unsigned int* counter)
 {
     sums_sync();
-    if (threadIdx.x == 32 * (CONSUMERS + 1 + AUX_WARPS + SPARE_WARPS)) {
+    if (threadIdx.x == 32 * FIRST_SUM) {
         __threadfence();
         atomicAdd(counter, 1u);
     }
@@ -1111,11 +1111,11 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(const __grid_constant__
         for (int i = 0; i < MAX_STAGES; ++i) {
             // the weights' bytes; the lanes that copy scale bytes; the records' bytes
             tc::mbar_init(smem_of(&sh.full[i]), 1u + (FMT == kF8 ? 0u : 32u) + 1u);
-            tc::mbar_init(smem_of(&sh.empty[i]), (uint32_t)CONSUMERS / 2u);
+            tc::mbar_init(smem_of(&sh.empty[i]), (uint32_t)SET);
         }
-        for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(smem_of(&sh.summable[i]), (uint32_t)CONSUMERS);
-            tc::mbar_init(smem_of(&sh.summed[i]), (uint32_t)SUM_WARPS);
+        for (int i = 0; i < 2 * STREAMS; ++i) {
+            tc::mbar_init(smem_of(&sh.summable[i / 2][i % 2]), (uint32_t)SET);
+            tc::mbar_init(smem_of(&sh.summed[i / 2][i % 2]), (uint32_t)SUM_WARPS);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.up.map)) : "memory");
@@ -1149,30 +1149,31 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(const __grid_constant__
     __syncthreads();
     make_plan<FMT>(p, sh);
 
-    if (warp < CONSUMERS) {
+    const int stream = warp < FIRST_COPY ? warp / SET : warp < FIRST_SUM ? (warp - FIRST_COPY) / 2 : (warp - FIRST_SUM) / SUM_WARPS;
+    Buffers buf{smem_of(sh.summed[stream]), smem_of(sh.summable[stream]), red + stream * (RED_BYTES / 4 / STREAMS),
+                sh.plan.buffers, 0, 0u};
+    if (warp < FIRST_COPY) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_PRODUCTS));
-        Cursor cur{smem_of(sh.full), smem_of(sh.empty), sh.plan.stages, 0, 0u, 0u, true};
-        Buffers buf{sh.plan.buffers, 0, 0u};
-        multiply<FMT, 0>(p, sh, ring, red, cur, buf);
-        multiply<FMT, 1>(p, sh, ring, red, cur, buf);
-    } else if (warp < CONSUMERS + 1 + AUX_WARPS + SPARE_WARPS) {
+        Cursor cur{smem_of(sh.full), smem_of(sh.empty), sh.plan.stages, stream, 0u, 0u, true};
+        multiply<FMT, 0>(p, sh, ring, stream, cur, buf);
+        multiply<FMT, 1>(p, sh, ring, stream, cur, buf);
+    } else if (warp < FIRST_SUM) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHERS));
-        if (warp == CONSUMERS) {
-            if ((threadIdx.x & 31) == 0) stream_weights<FMT>(p, sh, ring);
+        if (warp & 1) {
+            stream_aux<FMT>(p, sh, ring, stream);
+        } else {
+            if ((threadIdx.x & 31) == 0) stream_weights<FMT>(p, sh, ring, stream);
             __syncwarp();
-        } else if (warp < CONSUMERS + 1 + AUX_WARPS) {
-            stream_aux<FMT>(p, sh, ring, warp - CONSUMERS - 1);
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHERS));
-        Buffers buf{sh.plan.buffers, 0, 0u};
         bool live = true;
-        add_slices<FMT, 0>(p, sh, red, buf, live);
+        add_slices<FMT, 0>(p, sh, stream, buf, live);
         sums_count(&p.ctl->h_done);
         // the pairs' maxima are read directly, not through a stage
-        if (threadIdx.x == 32 * (CONSUMERS + 1 + AUX_WARPS + SPARE_WARPS)) spin(&p.ctl->h_done, gridDim.x, p.fault);
+        if (threadIdx.x == 32 * FIRST_SUM) spin(&p.ctl->h_done, gridDim.x, p.fault);
         sums_sync();
-        add_slices<FMT, 1>(p, sh, red, buf, live);
+        add_slices<FMT, 1>(p, sh, stream, buf, live);
         sums_count(&p.ctl->o_done);
     }
     __syncthreads();
