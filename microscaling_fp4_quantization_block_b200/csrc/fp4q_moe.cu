@@ -29,12 +29,13 @@
 // of more than 8 pairs are near its bound.
 //
 // Measured (graph replays; the experts' bytes at the copy rate of 6.55 TB/s in
-// brackets): 1 token, 8 of 64 NVFP4 experts of 2048 x 1024, 29 us (4.4): launch,
+// brackets): 1 token, 8 of 64 NVFP4 experts of 2048 x 1024, 28 us (4.4): launch,
 // router, choices and the three waits take 17 of them; 5 tokens over E4M3 experts
-// 59 us (26); 64 tokens over 128 MXFP4 experts of 2048 x 768 176 us (48); over 64
-// NVFP4 experts of 5120 x 1792 319 us (152).  What bounds the long calls is the
-// product warps' work per stage (about 1 us of latencies for 16 KB of codes) and
-// the warps that fill the stages; with the products left out the last takes 245.
+// 55 us (26); 23 tokens over 60 NVFP4 experts 62 us (24); 64 tokens over 128 MXFP4
+// experts of 2048 x 768 127 us (48); over 64 NVFP4 experts of 5120 x 1792 299 us
+// (152).  With the products left out these take 25, 51, 51, 95 and 215 us: what
+// bounds the long calls is the products' instructions on top of a stream of 4 to
+// 5 TB/s that the warps filling the stages sustain.
 //
 // Activations enter the products as fp16 under one power of two per row (the
 // row's largest value in [2^7, 2^8)): bf16 inputs keep every bit down to 2^-24
