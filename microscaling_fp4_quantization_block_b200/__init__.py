@@ -125,10 +125,10 @@ def _need_cuda(*ts):
 
 
 def _one_device(*ts) -> None:
-    """Checks that the given tensors live on the current CUDA device."""
-    index = torch._C._cuda_getDevice()
+    """Checks that the given tensors live on the first one's CUDA device."""
+    index = ts[0].get_device()
     for t in ts:
-        if t is not None and t.get_device() != index:
+        if t is not None and (index < 0 or t.get_device() != index):
             raise ValueError("fp4q tensors of one call must live on one CUDA device")
 
 

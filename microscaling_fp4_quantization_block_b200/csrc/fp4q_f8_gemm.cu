@@ -15,11 +15,16 @@
 //     b + 1 runs while block b is drained.  One thread alone took 650 clocks a
 //     block for its two waits and two commits, more than the 512 of the MMAs;
 //   warps 4-11: two groups of four, each draining half the columns: a thread
-//     owns a row of y (a lane of tensor memory) and BN / 2 columns, the scale
-//     is one number per thread and block, and pairs of columns are scaled and
-//     added by one packed fused multiply-add.
+//     owns a row of y (a lane of tensor memory) and BN / 2 columns, and the scale
+//     is one number per thread and block.
+// For few rows of A a second kernel (below) puts B's rows on the lanes instead.
 // Every wait is bounded; a wait that runs out records the library's fault word
 // and the CTA stops its work and returns.
+//
+// Measured (graph replays): 8192 x 13824 x 5120 567 us, 2.05 PFLOP/s (0.62 of
+// twice the measured bf16 rate; 490 us with the accumulators left unread); 1 x
+// 13824 x 5120 18.8 us (its bytes at the copy rate: 10.8); 37 x 3584 x 18944 20.8
+// (10.5).
 #include <cuda.h>
 #include <cuda_bf16.h>
 

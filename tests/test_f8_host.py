@@ -86,3 +86,22 @@ def test_moe_rejects_bad_arguments(L):
     need = L.fp4q_moe_workspace_size(2, 128, 128, 8, 2)
     assert need > 0 and call(ws_bytes=need - 1) == -6
     assert L.fp4q_moe_workspace_size(65, 128, 128, 8, 2) == 0
+
+
+def test_the_binding_refuses_cpu_tensors_and_wrong_shapes(L):
+    """Checked before the library or a device is asked."""
+    import torch
+
+    import microscaling_fp4_quantization_block_b200 as m
+    x = torch.zeros((4, 128), dtype=torch.bfloat16)
+    codes, scales = torch.zeros((4, 128), dtype=torch.uint8), torch.ones((4, 1))
+    with pytest.raises(ValueError):
+        m.fp4q_f8_quantize(x)
+    with pytest.raises(ValueError):
+        m.fp4q_f8_quantize(x.float())
+    with pytest.raises(ValueError):
+        m.fp4q_f8_gemm(codes, scales, codes, scales[:1])
+    with pytest.raises(ValueError):
+        m.fp4q_moe(x, x, 2, (codes, scales, None), (codes, scales, None), "mxfp4")
+    with pytest.raises(ValueError):
+        m.fp4q_moe(x, x, 2, (codes, scales, None), (codes, scales, None), "e8m0")

@@ -246,3 +246,29 @@ def test_gemm_empty_and_refusals(fq):
         fq.fp4q_f8_gemm(a, sa, b, sb, y=torch.empty((8, 4), dtype=torch.bfloat16, device="cuda"))
     with pytest.raises(fq.Fp4qError):
         fq.fp4q_f8_gemm(a[:, :24].contiguous(), sa, b[:, :24].contiguous(), sb)
+
+
+def test_past_32_bits(fq):
+    """Operands and results of more than 2^31 values: every tile of the integers' product, bit for
+    bit where it is looked at (the first and last rows, and a sample between)."""
+    m, n, k = 70000, 33024, 128
+    g = torch.Generator(device="cuda").manual_seed(3)
+    a = torch.randint(-8, 9, (m, k), generator=g, device="cuda").float()
+    b = torch.randint(-8, 9, (n, k), generator=g, device="cuda").float()
+    sa = torch.exp2(torch.randint(-2, 3, (m, 1), generator=g, device="cuda").float())
+    sb = torch.exp2(torch.randint(-2, 3, (-(-n // 128), 1), generator=g, device="cuda").float())
+    y = fq.fp4q_f8_gemm(a.to(torch.float8_e4m3fn), sa, b.to(torch.float8_e4m3fn), sb)
+    rows = torch.cat([torch.arange(3), torch.randint(0, m, (200,)), torch.arange(m - 3, m)]).cuda()
+    want = (a[rows].double() * sa[rows].double()) @ (b.double() * sb.double().repeat_interleave(128, 0)[:n]).T
+    assert torch.equal(y[rows].double(), want.to(torch.bfloat16).double())
+    # the result as an input: rows past the 2^31st value quantized like any other
+    c, s = fq.fp4q_f8_quantize(y, ROW)
+    last = y[-130:].clone()
+    wc, ws = fq.fp4q_f8_quantize(last, ROW)
+    assert torch.equal(c[-130:].view(torch.uint8), wc.view(torch.uint8)) and torch.equal(s[-130:], ws)
+    wc, ws = quantize_oracle(last[-4:], ROW)
+    assert same(c[-4:], wc) and same(s[-4:], ws)
+    c, s = fq.fp4q_f8_quantize(y, TILE)
+    wc, ws = quantize_oracle(y[m // 128 * 128:].cpu(), TILE)
+    assert same(c[m // 128 * 128:], wc) and same(s[-1:], ws)
+    assert fq.fp4q_device_fault() == 0

@@ -292,6 +292,28 @@ def test_workspace_graphs_streams_and_outputs(fq):
     assert fq.fp4q_device_fault() == 0
 
 
+def test_past_32_bits(fq):
+    """Codes of more than 2^32 bytes: the first, a middle and the last of 512 wide experts."""
+    experts, hidden, inter = 512, 5120, 2048
+    g = torch.Generator(device="cuda").manual_seed(4)
+    draw = lambda r, c: torch.randint(0, 256, (r, c), generator=g, device="cuda", dtype=torch.uint8)
+    scale = lambda r, c: torch.randint(118, 124, (r, c), generator=g, device="cuda", dtype=torch.uint8)
+    up = (draw(experts * 2 * inter, hidden // 2), scale(experts * 2 * inter, hidden // 32), None)
+    down = (draw(experts * hidden, inter // 2), scale(experts * hidden, inter // 32), None)
+    assert up[0].numel() > 2 ** 32
+    ids = torch.tensor([[511, 0], [400, 511], [255, 409]], dtype=torch.int32)
+    w = torch.tensor([[0.5, 0.25], [0.75, 1.0], [0.3, 0.6]])
+    x = workloads.gaussian_bf16(3, hidden, 2.0 ** -6, 5, device="cuda")
+    y, _, _ = fq.fp4q_moe(x, None, 2, up, down, "mxfp4", ids=ids.cuda(), weights=w.cuda())
+    torch.cuda.synchronize()
+    chosen = sorted(set(ids.flatten().tolist()))
+    part = lambda m, r: tuple(t.view(experts, r, -1)[chosen].flatten(0, 1) for t in m[:2])
+    few = torch.tensor([[chosen.index(e) for e in row] for row in ids.tolist()])
+    check_y(y, x, decode(part(up, 2 * inter), "mxfp4", len(chosen)), decode(part(down, hidden), "mxfp4", len(chosen)),
+            few, w)
+    assert fq.fp4q_device_fault() == 0
+
+
 def test_two_host_threads_on_two_streams(fq):
     """Layers, products for few and for many tokens, in turn on two streams of different
     priority, from two host threads at once, a workspace each."""
