@@ -177,6 +177,29 @@ def test_choices_made_elsewhere(fq, fmt, kind):
     assert not y.cpu()[nothing].any()
 
 
+@pytest.mark.parametrize("tokens,top_k", [(1, 1), (1, 16), (8, 4), (2, 16), (7, 4), (11, 3)])
+@pytest.mark.parametrize("kind", ["any", "one expert", "some gone", "all gone"])
+def test_few_pairs(fq, tokens, top_k, kind):
+    """Up to 32 pairs, and just above: lists of one, of more than a group's 16, with gaps, empty."""
+    experts, hidden, inter = 20, 160, 96
+    g = torch.Generator().manual_seed(tokens * 31 + top_k)
+    ids = torch.randint(0, experts, (tokens, top_k), generator=g, dtype=torch.int32)
+    if kind == "one expert":
+        ids.fill_(19)
+    elif kind == "some gone":
+        ids[torch.rand((tokens, top_k), generator=g) < 0.5] = -7
+    elif kind == "all gone":
+        ids.fill_(20)
+    w = torch.rand((tokens, top_k), generator=g)
+    up = experts_of(fq, "nvfp4", experts, 2 * inter, hidden, 0.05, 1)
+    down = experts_of(fq, "nvfp4", experts, hidden, inter, 0.06, 2)
+    x = workloads.gaussian_bf16(tokens, hidden, 1.0, 3, device="cuda")
+    y, _, _ = fq.fp4q_moe(x, None, top_k, up, down, "nvfp4", ids=ids.cuda(), weights=w.cuda())
+    torch.cuda.synchronize()
+    assert fq.fp4q_device_fault() == 0
+    check_y(y, x, decode(up, "nvfp4", experts), decode(down, "nvfp4", experts), ids, w)
+
+
 def test_equal_logits_take_the_lower_expert(fq):
     tokens, experts, top_k, hidden, inter = 4, 70, 5, 256, 64
     up = experts_of(fq, "nvfp4", experts, 2 * inter, hidden, 0.05, 1)
