@@ -91,6 +91,8 @@ __device__ __forceinline__ void encode16(const U32x8& w, float s, uint32_t (&out
 template <int U>
 __global__ void __launch_bounds__(THREADS) f8_rows_kernel(const Params p)
 {
+    pdl_wait();
+    pdl_release();
     const int lane = threadIdx.x & 31;
     const int64_t warp = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5);
     const int sub = lane / LANES, at = (lane % LANES) * VEC;
@@ -134,6 +136,8 @@ __global__ void __launch_bounds__(THREADS) f8_rows_kernel(const Params p)
 // 128 x 128 tiles: one CTA per tile, 16 rows per warp, 4 rows per load.
 __global__ void __launch_bounds__(THREADS) f8_tiles_kernel(const Params p)
 {
+    pdl_wait();
+    pdl_release();
     __shared__ uint32_t part[WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t tr = blockIdx.x / p.kb, tc = blockIdx.x - tr * p.kb;
@@ -186,12 +190,12 @@ extern "C" int fp4q_f8_quantize(const void* x, int64_t rows, int64_t cols, int g
         return FP4Q_ERR_ALIGN;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     f8::Params p{static_cast<const uint16_t*>(x), codes, scales, rows, cols, rows * kb, kb};
-    if (grain == FP4Q_F8_TILE) {
-        f8::f8_tiles_kernel<<<(unsigned)tiles, f8::THREADS, 0, s>>>(p);
-    } else if (p.groups <= 148 * 64) {
-        f8::f8_rows_kernel<1><<<(unsigned)((p.groups + 31) / 32), f8::THREADS, 0, s>>>(p);
-    } else {
-        f8::f8_rows_kernel<2><<<(unsigned)((p.groups + 63) / 64), f8::THREADS, 0, s>>>(p);
-    }
-    return cudaGetLastError() == cudaSuccess ? FP4Q_OK : FP4Q_ERR_CUDA;
+    cudaError_t e;
+    if (grain == FP4Q_F8_TILE)
+        e = launch_pdl(f8::f8_tiles_kernel, (int)tiles, f8::THREADS, 0, s, p);
+    else if (p.groups <= 148 * 64)
+        e = launch_pdl(f8::f8_rows_kernel<1>, (int)((p.groups + 31) / 32), f8::THREADS, 0, s, p);
+    else
+        e = launch_pdl(f8::f8_rows_kernel<2>, (int)((p.groups + 63) / 64), f8::THREADS, 0, s, p);
+    return e == cudaSuccess ? FP4Q_OK : FP4Q_ERR_CUDA;
 }

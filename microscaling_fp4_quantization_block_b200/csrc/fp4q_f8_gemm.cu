@@ -257,6 +257,8 @@ __global__ void __launch_bounds__(THREADS, 1) f8_gemm_kernel(const __grid_consta
     uint32_t tmem;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(slot) : "memory");
 
+    pdl_wait();                                              // what came before in the stream; the set-up above overlaps it
+    pdl_release();
     // tiles in m-fastest order: a wave of CTAs shares a few B tiles and streams A from L2
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_CONTROL));
@@ -336,8 +338,7 @@ int launch(Params& p, const uint8_t* b, int64_t k, cudaStream_t s)
     if (!make_byte_map(&p.tb, b, p.n, k, BN)) return FP4Q_ERR_CUDA;
     const int64_t tiles = ((p.m + BM - 1) / BM) * ((p.n + BN - 1) / BN);
     const int grid = grid_for((const void*)f8_gemm_kernel<BN>, Shape<BN>::SMEM_BYTES, tiles, THREADS);
-    f8_gemm_kernel<BN><<<grid, THREADS, Shape<BN>::SMEM_BYTES, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? FP4Q_OK : FP4Q_ERR_CUDA;
+    return launch_pdl(f8_gemm_kernel<BN>, grid, THREADS, Shape<BN>::SMEM_BYTES, s, p) == cudaSuccess ? FP4Q_OK : FP4Q_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------- few tokens
@@ -434,6 +435,8 @@ __global__ void __launch_bounds__(SMALL_THREADS, 2) f8_gemm_small_kernel(const _
     uint32_t tmem;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(slot) : "memory");
 
+    pdl_wait();
+    pdl_release();
     f32x2 acc[NTOK / 2];
     if (warp == 0 && lane == 0) {
         for (int i = 0, s = 0, ph = 1; i < nk; ++i) {
@@ -582,13 +585,15 @@ int launch_small(const Params& g, const uint8_t* a, const uint8_t* b, int64_t k,
     cfg.blockDim = dim3((unsigned)SMALL_THREADS);
     cfg.dynamicSmemBytes = Small<NTOK>::SMEM_BYTES;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)split;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, f8_gemm_small_kernel<NTOK>, p) == cudaSuccess ? FP4Q_OK : FP4Q_ERR_CUDA;
 }
 

@@ -361,7 +361,8 @@ __device__ void choose(const Params& p, Shared& sh, int first, int step, bool te
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) below += __shfl_xor_sync(0xffffffffu, below, d);
         }
-        uint32_t chosen = NONE, key_of = 0;                   // lane k: the k-th choice
+        float mine = 0.0f;
+        uint32_t chosen = NONE;
         for (int k = 0; k < p.top_k; ++k) {
             const uint32_t top = __reduce_max_sync(0xffffffffu, best);
             uint32_t at = NONE;                               // the first expert that has it
@@ -375,9 +376,11 @@ __device__ void choose(const Params& p, Shared& sh, int first, int step, bool te
                 if (at == (uint32_t)(lane + 32 * j)) key[j] = 0;
                 best = max(best, key[j]);
             }
-            if (lane == k) chosen = at, key_of = top;
+            if (lane == k) {
+                chosen = at;
+                mine = expf(from_ordered(top) - peak);
+            }
         }
-        const float mine = lane < p.top_k ? expf(from_ordered(key_of) - peak) : 0.0f;
         if (p.normalize) {
             below = mine;
 #pragma unroll
@@ -395,50 +398,12 @@ __device__ void choose(const Params& p, Shared& sh, int first, int step, bool te
     }
 }
 
-// The shape of a stage, for groups of up to `widest` pairs.
-template <int FMT>
-__device__ __forceinline__ void stage_shape(Plan& q, int groups, int widest)
-{
-    using F = Format<FMT>;
-    q.groups = groups;
-    q.widest = widest;
-    q.buffers = widest > 8 ? 1 : 2;
-    q.acts_at = TILE * F::SCALE_PITCH;
-    q.inverse_at = q.acts_at + widest * F::RECORD;
-    q.aux_bytes = (q.inverse_at + widest * 4 + 15u) & ~15u;
-    q.stages = min(MAX_STAGES, (int)(RING_BYTES / (WEIGHT_BYTES + q.aux_bytes))) & ~1;
-}
-
 // The pairs by expert, the groups, and the shape of a stage.
 template <int FMT>
 __device__ void make_plan(const Params& p, Shared& sh)
 {
+    using F = Format<FMT>;
     const int pairs = p.tokens * p.top_k, lane = threadIdx.x & 31;
-    if (pairs <= 32) {
-        // one warp, a lane per pair: experts in the order of their first pair
-        if (threadIdx.x < 32) {
-            const uint32_t e = lane < pairs ? sh.id[lane] : NONE;
-            const uint32_t same = __match_any_sync(0xffffffffu, e), before = same & ((1u << lane) - 1u);
-            const int n = e != NONE && before == 0u ? __popc(same) : 0, ng = (n + GROUP - 1) / GROUP;    // the first pair's lane
-            int sn = n, sg = ng;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, sn, d), v = __shfl_up_sync(0xffffffffu, sg, d);
-                if (lane >= d) sn += u, sg += v;
-            }
-            const int at = __shfl_sync(0xffffffffu, sn - n, __ffs(same) - 1);
-            if (e != NONE) sh.list[at + __popc(before)] = (uint16_t)lane;
-            for (int i = 0; i < ng; ++i) {
-                sh.g_expert[sg - ng + i] = (uint16_t)e;
-                sh.g_first[sg - ng + i] = (uint16_t)(at + i * GROUP);
-                sh.g_count[sg - ng + i] = (uint8_t)min(GROUP, n - i * GROUP);
-            }
-            const int widest = __reduce_max_sync(0xffffffffu, min(GROUP, n));
-            if (lane == 31) stage_shape<FMT>(sh.plan, sg, widest);
-        }
-        __syncthreads();
-        return;
-    }
     for (int e = threadIdx.x; e < p.experts; e += THREADS) sh.count[e] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < pairs; i += THREADS)
@@ -470,7 +435,16 @@ __device__ void make_plan(const Params& p, Shared& sh)
         }
         if (lane == 0) sh.first[p.experts] = (uint16_t)total;
         widest = __reduce_max_sync(0xffffffffu, widest);
-        if (lane == 0) stage_shape<FMT>(sh.plan, groups, widest);
+        if (lane == 0) {
+            Plan& q = sh.plan;
+            q.groups = groups;
+            q.widest = widest;
+            q.buffers = widest > 8 ? 1 : 2;
+            q.acts_at = TILE * F::SCALE_PITCH;
+            q.inverse_at = q.acts_at + widest * F::RECORD;
+            q.aux_bytes = (q.inverse_at + widest * 4 + 15u) & ~15u;
+            q.stages = min(MAX_STAGES, (int)(RING_BYTES / (WEIGHT_BYTES + q.aux_bytes))) & ~1;
+        }
     }
     __syncthreads();
     // Within a group the order of the pairs changes nothing; which group a pair
