@@ -878,11 +878,12 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
             } else {
                 constexpr int PIECES = FMT == kNv ? 4 : 2;   // 16-byte pieces of activations per lane
                 uint4 bf[NT][PIECES], w[2][2];               // all loads first
+                const uint32_t wa = w0 + ((uint32_t)((c16 + t) ^ rho) << 4);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint32_t wa = w0 + (uint32_t)(i * BOX_BYTES) + ((uint32_t)((c16 + t) ^ rho) << 4);
-                    w[i][0] = lds128(wa);
-                    w[i][1] = lds128(wa + 1024u);
+                    if (NT > 1 && i > 0) break;              // (of one box at a time with two tiles of columns: registers)
+                    w[i][0] = lds128(wa + (uint32_t)(i * BOX_BYTES));
+                    w[i][1] = lds128(wa + (uint32_t)(i * BOX_BYTES + 1024));
                 }
                 uint32_t two[2][2];                          // NVFP4: two scale bytes per row and block
                 if constexpr (FMT == kNv) {
@@ -909,7 +910,7 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint4 v0 = w[i][0], v1 = w[i][1];
+                    const uint4 v0 = w[NT > 1 ? 0 : i][0], v1 = w[NT > 1 ? 0 : i][1];
                     const uint32_t u0[4] = {v0.x, v0.y, v0.z, v0.w}, u1[4] = {v1.x, v1.y, v1.z, v1.w};
                     if constexpr (FMT == kNv) {
                         uint32_t m[2][2];                    // two scales per row and block
@@ -955,6 +956,10 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
                         for (int c = 0; c < NT; ++c)
 #pragma unroll
                             for (int j = 0; j < 4; ++j) acc[i][c][j] = __fmaf_rn(d[c][j], fs[i], acc[i][c][j]);
+                    }
+                    if (NT > 1 && i == 0) {
+                        w[0][0] = lds128(wa + BOX_BYTES);
+                        w[0][1] = lds128(wa + BOX_BYTES + 1024u);
                     }
                 }
             }
