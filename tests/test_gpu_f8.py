@@ -167,6 +167,12 @@ def test_gemm_exact_on_integers(fq, m, n, k):
     assert fq.fp4q_device_fault() == 0
 
 
+@pytest.mark.parametrize("m,n,k", [(2049, 3001, 128), (2300, 2200, 272), (6200, 1030, 144), (40000, 70, 144), (200, 40000, 144)])
+def test_gemm_bands_of_tiles(fq, m, n, k):
+    """Tiles are walked in bands of 16 rows of tiles: a last band of one, two and fewer rows than a band, one column, one band."""
+    test_gemm_exact_on_integers(fq, m, n, k)
+
+
 @pytest.mark.parametrize("m", [1, 40, 200])
 def test_gemm_keeps_rows_apart(fq, m):
     """A row of A, or of B, that holds NaN or an infinite scale changes its own row, or column, alone."""
