@@ -797,7 +797,8 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
         const int s = cur.slot;
         const uint32_t ph = cur.phase;
         if ((cur.slot += STREAMS) >= cur.stages) cur.slot -= cur.stages, cur.phase ^= 1u;
-        const int qi = (int)(((uint32_t)warp + cur.seq++) & 3u);       // turns, so that short stages load all alike
+        // turns, also from one item to the next, so that short stages load all warps alike (whose partial sums these are: item_products)
+        const int qi = (int)(((uint32_t)warp + cur.seq++) & 3u);
         const int values = min(F::VALUES, f.k - k0);
         float fs[2] = {};
         if (FMT == kF8 && qi * F::QUARTER < values) {
@@ -987,12 +988,15 @@ __device__ __forceinline__ void item_products(const Params& p, const Shared& sh,
                                               int n, Cursor& cur, Buffers& buf)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // The slice is the quarter that the warp takes of the item's first stage: what a slice holds, and so the order
+    // of the sums, does not depend on how many stages the stream has been through.
+    const int slice = (int)(((uint32_t)warp + cur.seq) & 3u);
     float acc[2][NT][4] = {};
     item<FMT, NT, WHICH>(p, sh.plan, ring, f, row0, n, cur, acc);
 
     const int g = lane >> 2, t = lane & 3, half = (warp >> 2) & 1;
     constexpr int PITCH = 8 * NT + 1;                        // floats per row of the partial sums
-    const int slice = warp & 3, rho = (g >> 1) | ((g & 1) << 2);
+    const int rho = (g >> 1) | ((g & 1) << 2);
     if (cur.live) cur.live = __all_sync(0xffffffffu, tc::wait_phase(buf.summed + 8u * buf.at, buf.phase ^ 1u, p.fault));
     float* to = buf.sums + (buf.at * SLICES * TILE + slice * TILE + 16 * half + rho) * PITCH + 2 * t;
 #pragma unroll

@@ -423,3 +423,24 @@ def test_empty_and_refusals(fq):
                                     weights=torch.zeros((2, 2), device="cuda"))):
         with pytest.raises(ValueError):
             bad()
+
+
+@pytest.mark.parametrize("fmt,experts,hidden,inter", [
+    ("nvfp4", 64, 5120, 768), ("nvfp4", 60, 1440, 1376), ("mxfp4", 128, 2048, 768), ("mxfp4", 60, 1440, 1376),
+    ("f8", 32, 4096, 896), ("f8", 24, 1408, 1664)])
+def test_a_token_alone_and_among_others(fq, fmt, experts, hidden, inter):
+    """A token's result does not depend on who else is there, bit for bit, where a CTA works through many items
+    whose stages are no multiple of the slices of k."""
+    tokens, top_k = 64, 8
+    up = experts_of(fq, fmt, experts, 2 * inter, hidden, hidden ** -0.5, 1)
+    down = experts_of(fq, fmt, experts, hidden, inter, inter ** -0.5, 2)
+    router = workloads.gaussian_bf16(experts, hidden, hidden ** -0.5, 3, device="cuda")
+    x = workloads.gaussian_bf16(tokens, hidden, 1.0, 4, device="cuda")
+    y, ids, w = fq.fp4q_moe(x, router, top_k, up, down, fmt)
+    differ = []
+    for first, last in ((0, 1), (17, 18), (63, 64), (5, 7), (30, 41), (8, 48)):
+        ya, ia, wa = fq.fp4q_moe(x[first:last], router, top_k, up, down, fmt)
+        assert torch.equal(ia, ids[first:last]) and torch.equal(wa, w[first:last])
+        differ.append(int((ya != y[first:last]).sum()))
+    assert not any(differ), differ
+    assert fq.fp4q_device_fault() == 0
