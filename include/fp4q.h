@@ -511,7 +511,7 @@ FP4Q_API int fp4q_f8_gemm(const uint8_t* codes_a, const float* scales_a, int64_t
  * hidden and inter: multiples of 32 (128 for FP4Q_F8_BLOCK128), FP4Q_ERR_SHAPE
  * otherwise, at most 65536; experts, top_k at most FP4Q_MOE_MAX_EXPERTS,
  * FP4Q_MOE_MAX_TOPK and top_k at most experts: FP4Q_ERR_UNSUPPORTED.  x, y,
- * router, codes, scales 16-byte aligned.  Logits are fp32 sums; inside the
+ * router, codes, scales 16-byte aligned.  Logits are 64-bit sums; inside the
  * products x is exact to 2^-25 of the largest of each 32 values, h has 11
  * significant bits, sums are fp32 in a fixed order, and y is rounded once.
  * The launch is cooperative: one CTA on every SM.  Enqueued on `stream`.

@@ -111,7 +111,7 @@ struct Params {
     float* weights;
     uint16_t* y;                    // bf16 [tokens][hidden]
     Control* ctl;
-    float* logits;                  // [slices of k][tokens][experts]
+    double* logits;                 // [slices of k][tokens][experts]
     uint8_t* xs;                    // [tokens][xstages] records (Format::RECORD bytes)
     float* xpow;                    // [tokens]
     uint8_t* h;                     // [pairs][hstages] records
@@ -267,68 +267,123 @@ __device__ __forceinline__ int logit_slices(const Params& p)
     return max(1, min(min(8, p.hidden / 256), (int)gridDim.x * (THREADS / 32) / p.experts));
 }
 
-// One task: expert e against N tokens from t0 (those past `last` repeat it), fp32 products and sums.
-template <int N>
-__device__ __forceinline__ void logits_of(const Params& p, int e, int t0, int from, int to, float* out)
+// The sums over the warp's lanes of COUNT values each, by halves: lane l ends up
+// with value l / (32 / COUNT).  Whatever COUNT, a value's sum is the same tree.
+template <int COUNT>
+__device__ __forceinline__ double lane_sums(double (&v)[COUNT])
 {
-    const int lane = threadIdx.x & 31, last = p.tokens - 1;
-    const uint16_t* r = p.router + (int64_t)e * p.hidden;
-    float s[N] = {};
-#pragma unroll 2
-    for (int c = from + lane * 8; c < to; c += 256) {
-        uint4 b[N];
-        const uint4 a = *reinterpret_cast<const uint4*>(r + c);
+    const int lane = threadIdx.x & 31;
+    int n = COUNT;
 #pragma unroll
-        for (int t = 0; t < N; ++t) b[t] = *reinterpret_cast<const uint4*>(p.x + (int64_t)min(t0 + t, last) * p.hidden + c);
-        const uint32_t av[4] = {a.x, a.y, a.z, a.w};
+    for (int d = 16; d > 0; d >>= 1) {
+        if (n > 1) {
+            n /= 2;
+            const bool upper = (lane & d) != 0;
 #pragma unroll
-        for (int t = 0; t < N; ++t) {
-            const uint32_t bv[4] = {b[t].x, b[t].y, b[t].z, b[t].w};
+            for (int i = 0; i < COUNT / 2; ++i)
+                if (i < n) {
+                    const double mine = upper ? v[i + n] : v[i], other = upper ? v[i] : v[i + n];
+                    v[i] = mine + __shfl_xor_sync(0xffffffffu, other, d);
+                }
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], d);
+        }
+    }
+    return v[0];
+}
+
+// One task: E experts from e0 against N tokens from t0 (those past the last
+// repeat it).  The sums are held in 64 bits, where a product of two bf16 values
+// is exact: which of two nearly equal logits is the larger decides a token's
+// experts, and fp32 sums of equal logits differ.
+template <int E, int N>
+__device__ __forceinline__ void logits_of(const Params& p, int e0, int t0, int from, int to, double* out)
+{
+    constexpr int W = E * N > 8 ? 4 : 8;                     // values of a row at a time: registers
+    const int lane = threadIdx.x & 31, last_t = p.tokens - 1, last_e = p.experts - 1;
+    double s[E * N] = {};
+    for (int c0 = from + lane * 8; c0 < to; c0 += 256) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                s[t] = __fmaf_rn(bf16_lo(av[j]), bf16_lo(bv[j]), s[t]);
-                s[t] = __fmaf_rn(bf16_hi(av[j]), bf16_hi(bv[j]), s[t]);
+        for (int c = c0; c < c0 + 8; c += W) {
+            uint32_t a[E][W / 2], b[N][W / 2];
+            auto load = [&](uint32_t (&v)[W / 2], const uint16_t* from_row) {
+                if constexpr (W == 8) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(from_row + c);
+                    v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+                } else {
+                    const uint2 u = *reinterpret_cast<const uint2*>(from_row + c);
+                    v[0] = u.x, v[1] = u.y;
+                }
+            };
+#pragma unroll
+            for (int e = 0; e < E; ++e) load(a[e], p.router + (int64_t)min(e0 + e, last_e) * p.hidden);
+#pragma unroll
+            for (int t = 0; t < N; ++t) load(b[t], p.x + (int64_t)min(t0 + t, last_t) * p.hidden);
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                double av[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) av[e] = (double)(j & 1 ? bf16_hi(a[e][j / 2]) : bf16_lo(a[e][j / 2]));
+#pragma unroll
+                for (int t = 0; t < N; ++t) {
+                    const double bv = (double)(j & 1 ? bf16_hi(b[t][j / 2]) : bf16_lo(b[t][j / 2]));
+#pragma unroll
+                    for (int e = 0; e < E; ++e) s[e * N + t] = __fma_rn(av[e], bv, s[e * N + t]);
+                }
             }
         }
     }
-#pragma unroll
-    for (int t = 0; t < N; ++t) {
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) s[t] += __shfl_xor_sync(0xffffffffu, s[t], d);
-        if (lane == 0 && t0 + t <= last) out[(t0 + t) * p.experts + e] = s[t];
-    }
+    const double sum = lane_sums<E * N>(s);
+    constexpr int LANES = 32 / (E * N);                      // that hold the same sum
+    const int i = lane / LANES, e = e0 + i / N, t = t0 + i % N;
+    if (lane % LANES == 0 && e <= last_e && t <= last_t) out[t * p.experts + e] = sum;
 }
 
-// Logits: a warp per (expert, up to 8 tokens, slice of k); the slices are added by their reader, in order.
+// Logits: a warp per (expert, up to 8 tokens, slice of k), or two experts where
+// that still gives every warp a task (x is widened to 64 bits half as often);
+// the slices are added by their reader, in order.
 __device__ void route_logits(const Params& p)
 {
-    const int warp = threadIdx.x >> 5;
-    const int per = (p.tokens + 7) / 8, slices = logit_slices(p), tasks = p.experts * per * slices;
+    const int warp = threadIdx.x >> 5, warps = (int)gridDim.x * (THREADS / 32);
+    const int per = (p.tokens + 7) / 8, slices = logit_slices(p);
     const int step = ((p.hidden + slices - 1) / slices + 7) & ~7;
-    for (int task = warp * gridDim.x + blockIdx.x; task < tasks; task += gridDim.x * (THREADS / 32)) {
+    const bool pairs = p.tokens > 4 && p.experts * per * slices > warps;
+    const int tasks = (pairs ? (p.experts + 1) / 2 : p.experts) * per * slices;
+    for (int task = warp * gridDim.x + blockIdx.x; task < tasks; task += warps) {
         const int u = task / slices, k = task - u * slices, e = u / per, t0 = (u - e * per) * 8;
         const int from = k * step, to = min(p.hidden, from + step);
-        float* out = p.logits + (int64_t)k * p.tokens * p.experts;
-        if (p.tokens - t0 == 1)
-            logits_of<1>(p, e, t0, from, to, out);
+        double* out = p.logits + (int64_t)k * p.tokens * p.experts;
+        if (pairs)
+            logits_of<2, 8>(p, 2 * e, t0, from, to, out);
+        else if (p.tokens - t0 == 1)
+            logits_of<1, 1>(p, e, t0, from, to, out);
         else if (p.tokens - t0 <= 4)
-            logits_of<4>(p, e, t0, from, to, out);
+            logits_of<1, 4>(p, e, t0, from, to, out);
         else
-            logits_of<8>(p, e, t0, from, to, out);
+            logits_of<1, 8>(p, e, t0, from, to, out);
     }
 }
 
-// An order of fp32 values in which NaN is the largest: larger pattern, larger value.
-__device__ __forceinline__ uint32_t ordered(float v)
+// An order of 64-bit values in which NaN is the largest: larger pattern, larger value.
+typedef unsigned long long Key;
+constexpr Key kNanKey = ~0ull;
+
+__device__ __forceinline__ Key ordered(double v)
 {
-    const uint32_t b = as_u32(v);
-    if ((b & 0x7fffffffu) > 0x7f800000u) return 0xffffffffu;
-    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+    const Key b = (Key)__double_as_longlong(v);
+    if ((b & ~(1ull << 63)) > 0x7ff0000000000000ull) return kNanKey;
+    return (b >> 63) ? ~b : b | 1ull << 63;
 }
 
-__device__ __forceinline__ float from_ordered(uint32_t k)
+__device__ __forceinline__ double from_ordered(Key k)
 {
-    return as_f32(k == 0xffffffffu ? 0x7fc00000u : (k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+    return __longlong_as_double((long long)(k == kNanKey ? 0x7ff8000000000000ull : (k >> 63) ? k ^ (1ull << 63) : ~k));
+}
+
+__device__ __forceinline__ Key warp_max(Key k)
+{
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32));
+    return (Key)hi << 32 | __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
 }
 
 // The top_k experts of every token and their weights, a warp per token; a lane holds PER experts.
@@ -337,34 +392,34 @@ __device__ void choose(const Params& p, Shared& sh, int first, int step, bool te
 {
     const int lane = threadIdx.x & 31, slices = logit_slices(p);
     for (int t = first; t < p.tokens; t += step) {
-        uint32_t key[PER];
+        Key key[PER];
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
             const int e = lane + 32 * j;
-            float part[8], v = 0.0f;
+            double part[8], v = 0.0;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                part[k] = e < p.experts && k < slices ? __ldcg(p.logits + ((int64_t)k * p.tokens + t) * p.experts + e) : 0.0f;
+                part[k] = e < p.experts && k < slices ? __ldcg(p.logits + ((int64_t)k * p.tokens + t) * p.experts + e) : 0.0;
 #pragma unroll
             for (int k = 0; k < 8; ++k) v += part[k];
-            key[j] = e < p.experts ? ordered(v) : 0u;         // an expert's is at least 0x007fffff: 0 marks what is gone
+            key[j] = e < p.experts ? ordered(v) : 0u;         // an expert's is at least 2^52 - 1: 0 marks what is gone
         }
-        uint32_t best = 0;
+        Key best = 0;
 #pragma unroll
         for (int j = 0; j < PER; ++j) best = max(best, key[j]);
-        const float peak = from_ordered(__reduce_max_sync(0xffffffffu, best));
+        const double peak = from_ordered(warp_max(best));
         float below = 0.0f;
         if (!p.normalize) {
 #pragma unroll
             for (int j = 0; j < PER; ++j)
-                if (lane + 32 * j < p.experts) below += expf(from_ordered(key[j]) - peak);
+                if (lane + 32 * j < p.experts) below += expf((float)(from_ordered(key[j]) - peak));
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) below += __shfl_xor_sync(0xffffffffu, below, d);
         }
         float mine = 0.0f;
         uint32_t chosen = NONE;
         for (int k = 0; k < p.top_k; ++k) {
-            const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+            const Key top = warp_max(best);
             uint32_t at = NONE;                               // the first expert that has it
 #pragma unroll
             for (int j = PER - 1; j >= 0; --j)
@@ -378,7 +433,7 @@ __device__ void choose(const Params& p, Shared& sh, int first, int step, bool te
             }
             if (lane == k) {
                 chosen = at;
-                mine = expf(from_ordered(top) - peak);
+                mine = expf((float)(from_ordered(top) - peak));
             }
         }
         if (p.normalize) {
@@ -1237,7 +1292,7 @@ Layout layout(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, in
     const int64_t pairs = tokens * top_k, rec = record_bytes(fmt);
     Layout l;
     l.logits = 256;
-    l.xs = l.logits + up(8 * tokens * experts * 4);
+    l.xs = l.logits + up(8 * tokens * experts * 8);
     l.xpow = l.xs + up(tokens * stages_of(hidden, fmt) * rec);
     l.h = l.xpow + up(tokens * 4);
     l.hmax = l.h + up(pairs * stages_of(inter, fmt) * rec);
@@ -1331,7 +1386,7 @@ extern "C" int fp4q_moe(const void* x, int64_t tokens, int64_t hidden, int64_t i
     p.y = static_cast<uint16_t*>(y);
     char* ws = static_cast<char*>(workspace);
     p.ctl = reinterpret_cast<Control*>(ws);
-    p.logits = reinterpret_cast<float*>(ws + l.logits);
+    p.logits = reinterpret_cast<double*>(ws + l.logits);
     p.xs = reinterpret_cast<uint8_t*>(ws + l.xs);
     p.xpow = reinterpret_cast<float*>(ws + l.xpow);
     p.h = reinterpret_cast<uint8_t*>(ws + l.h);

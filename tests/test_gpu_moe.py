@@ -444,3 +444,31 @@ def test_a_token_alone_and_among_others(fq, fmt, experts, hidden, inter):
         differ.append(int((ya != y[first:last]).sum()))
     assert not any(differ), differ
     assert fq.fp4q_device_fault() == 0
+
+
+@pytest.mark.parametrize("tokens,experts,top_k", [(1, 70, 5), (5, 512, 16), (64, 70, 8), (64, 512, 16), (9, 13, 13)])
+def test_close_logits_are_told_apart(fq, tokens, experts, top_k):
+    """Rows of the router that hold the same integers times powers of two in another order: the exact logits are
+    equal (42 bits, so 64-bit sums in any order are exact) where fp32 sums are not. Equal ones take the lower expert
+    and the same weight; ones that differ by a few 2^-12 of sums near 2^20 are in their exact order."""
+    hidden, inter = 2048, 32
+    g = torch.Generator().manual_seed(tokens + experts)
+    base = (2 * torch.randint(-64, 64, (hidden,), generator=g) + 1) * torch.exp2(torch.randint(-12, 13, (hidden,), generator=g).float())
+    base[0] = 0.0
+    sign = torch.where(torch.rand((hidden,), generator=g) < 0.5, -1.0, 1.0)
+    rows = torch.stack([torch.cat([base[:1], base[1:][torch.randperm(hidden - 1, generator=g)]]) for _ in range(experts)])
+    router = (rows * sign).bfloat16().cuda()
+    x = (sign * torch.exp2(-torch.randint(0, 9, (tokens, 1), generator=g).float() - 12)).bfloat16().cuda()
+    up = experts_of(fq, "mxfp4", experts, 2 * inter, hidden, 0.02, 1)
+    down = experts_of(fq, "mxfp4", experts, hidden, inter, 0.02, 2)
+    _, ids, w = fq.fp4q_moe(x, router, top_k, up, down, "mxfp4")
+    assert torch.equal(ids.cpu(), torch.arange(top_k, dtype=torch.int32).repeat(tokens, 1))
+    assert bool((w == w[0, 0]).all())
+    # column 0, where the rows hold nothing: different small integers (at most 255, in bf16 exactly) over 2^12
+    d = torch.randperm(experts, generator=g) % 256
+    router[:, 0] = (d * 2.0 ** -12 * sign[0]).bfloat16().cuda()
+    _, ids, _ = fq.fp4q_moe(x, router, top_k, up, down, "mxfp4")
+    want = torch.sort(d, descending=True, stable=True).indices[:top_k].to(torch.int32)
+    assert torch.equal(ids.cpu(), want.repeat(tokens, 1))
+    assert torch.equal(router.double().cpu() @ x.double().cpu().T, router.double().cpu().flip(1) @ x.double().cpu().flip(1).T)
+    assert fq.fp4q_device_fault() == 0
