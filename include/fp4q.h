@@ -514,6 +514,11 @@ FP4Q_API int fp4q_f8_gemm(const uint8_t* codes_a, const float* scales_a, int64_t
  * router, codes, scales 16-byte aligned.  Logits are 64-bit sums; inside the
  * products x is exact to 2^-25 of the largest of each 32 values, h has 11
  * significant bits, sums are fp32 in a fixed order, and y is rounded once.
+ * Scale bytes that are NaN (E8M0 255; UE4M3 from 0x7F on) make every result
+ * that takes them NaN.  The sums are formed before G and the power of two that
+ * a row of x or h is kept under: weights (codes times scales) whose magnitudes
+ * add up to 2^119 or more along a row overflow them, and ones below 2^-120
+ * lose bits.
  * The launch is cooperative: one CTA on every SM.  Enqueued on `stream`.
  */
 #define FP4Q_F8_BLOCK128 3             /* fmt of fp4q_moe: E4M3 with 128 x 128 scales */

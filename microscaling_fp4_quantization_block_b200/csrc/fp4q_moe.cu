@@ -733,12 +733,15 @@ __device__ __forceinline__ void mma16_zero(float (&d)[4], uint32_t a0, uint32_t 
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-// 2^(byte - 127) of byte b of four, as e8m0_decode but for 255, which is infinity here.
-template <int B>
-__device__ __forceinline__ float e8m0_byte(uint32_t four)
+// Four E8M0 scales as fp32 patterns' upper halves, two a word, in order: 2^(byte - 127), byte 255 NaN.
+__device__ __forceinline__ void e8m0_four(uint32_t four, uint32_t (&two)[2])
 {
-    const uint32_t at23 = B == 3 ? four >> 1 : four << (23 - 8 * B);
-    return as_f32(max(at23 & 0x7f800000u, 0x00400000u));
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.bf16x2.ue8m0x2 %0, l;\n\t"
+        "cvt.rn.bf16x2.ue8m0x2 %1, h;\n\t}"
+        : "=r"(two[0]), "=r"(two[1])
+        : "r"(four));
 }
 
 // Eight E2M1 codes -> four f16 pairs, in order.
@@ -768,9 +771,12 @@ __device__ __forceinline__ void widen8(uint32_t lo, uint32_t hi, uint32_t (&h)[4
         : "r"(lo), "r"(hi));
 }
 
-// Two UE4M3 bytes as f16.
+// Two UE4M3 bytes as f16.  The bytes from 0x7F on are NaN, as in ue4m3_decode: the conversion takes
+// a byte's top bit for a sign, so the bits below it are set.
 __device__ __forceinline__ uint32_t ue4m3_pair(uint32_t c)
 {
+    const uint32_t top = c & 0x8080u;
+    c |= top - (top >> 7);
     uint32_t h;
     asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(c));
     return h;
@@ -873,7 +879,7 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
 
             if constexpr (FMT == kMx) {
                 // four blocks of 32; a lane holds values 8 t .. 8 t + 7 of each
-                uint32_t sc[2][2];
+                uint32_t sc[2][2][2];                        // two scales a word
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -881,7 +887,7 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
                         const uint32_t at = aux + scale_at[i][r] + 4u * qi;
                         // four bytes that may straddle two words (one block may follow the last: not used)
                         const uint32_t lo = lds32(at & ~3u), hi = lds32((at & ~3u) + 4u * ((at & 3u) != 0u));
-                        sc[i][r] = __funnelshift_r(lo, hi, 8u * (at & 3u));
+                        e8m0_four(__funnelshift_r(lo, hi, 8u * (at & 3u)), sc[i][r]);
                     }
                 f32x2 ratio[NT][2];
                 if constexpr (WHICH == 1) {
@@ -916,7 +922,8 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
                         uint32_t a0[4], a1[4];
                         widen4(lds32(wb + (uint32_t)(i * BOX_BYTES)), a0);
                         widen4(lds32(wb + (uint32_t)(i * BOX_BYTES + 1024)), a1);
-                        const float s0 = e8m0_byte<b>(sc[i][0]), s1 = e8m0_byte<b>(sc[i][1]);
+                        const uint32_t p0 = sc[i][0][b >> 1], p1 = sc[i][1][b >> 1];
+                        const float s0 = b & 1 ? bf16_hi(p0) : bf16_lo(p0), s1 = b & 1 ? bf16_hi(p1) : bf16_lo(p1);
 #pragma unroll
                         for (int c = 0; c < NT; ++c) {
                             float d[4];

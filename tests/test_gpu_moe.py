@@ -472,3 +472,48 @@ def test_close_logits_are_told_apart(fq, tokens, experts, top_k):
     assert torch.equal(ids.cpu(), want.repeat(tokens, 1))
     assert torch.equal(router.double().cpu() @ x.double().cpu().T, router.double().cpu().flip(1) @ x.double().cpu().flip(1).T)
     assert fq.fp4q_device_fault() == 0
+
+
+@pytest.mark.parametrize("fmt,nan,tiny,huge", [("mxfp4", (0xFF,), 0, 254), ("nvfp4", (0x7F, 0x80, 0xB5, 0xFF), 0, 0x7E)])
+@pytest.mark.parametrize("tokens", [2, 40])
+def test_scale_bytes_at_the_ends(fq, fmt, nan, tiny, huge, tokens):
+    """The last scale bytes are NaN (as in fp4q_dequantize), the first the smallest scale, and the largest scale of a
+    block of zeros adds nothing; in every block of a row, which changes its own results alone."""
+    experts, top_k, hidden, inter = 3, 2, 544, 512
+    block = 32 if fmt == "mxfp4" else 16
+    up = experts_of(fq, fmt, experts, 2 * inter, hidden, 0.05, 1)
+    down = experts_of(fq, fmt, experts, hidden, inter, 0.05, 2)
+    x = workloads.gaussian_bf16(tokens, hidden, 1.0, 3, device="cuda")
+    ids = (torch.arange(tokens * 2, dtype=torch.int32).view(tokens, 2) % experts).cuda()
+    w = torch.full((tokens, 2), 0.5, device="cuda")
+    run = lambda u, d: fq.fp4q_moe(x, None, top_k, u, d, fmt, ids=ids, weights=w)[0]
+    clean = run(up, down)
+    hit = (ids == 1).any(1)                                  # tokens that read expert 1
+    blocks = inter // block
+    for byte in nan:
+        # row r of expert 1's down matrix, block r
+        s = down[1].clone()
+        at = torch.arange(blocks, device="cuda")
+        s[hidden + at, at] = byte
+        y = run(up, (down[0], s, down[2]))
+        assert bool(torch.isnan(y[hit][:, :blocks]).all())
+        assert torch.equal(y[~hit], clean[~hit]) and torch.equal(y[:, blocks:], clean[:, blocks:])
+        values = fq.fp4q_dequantize(down[0], s, down[2], experts * hidden, inter, fmt, block, 0, torch.float32)
+        assert bool(torch.isnan(values.view(-1, blocks, block)[hidden + at, at]).all())
+        # one gate row's block, then one up row's: a value of h, and with it the tokens' whole rows
+        for row in (2 * inter + 5, 3 * inter + 7):
+            for b in (0, 1, 7, hidden // block - 1):
+                s = up[1].clone()
+                s[row, b] = byte
+                y = run((up[0], s, up[2]), down)
+                assert bool(torch.isnan(y[hit]).all()) and torch.equal(y[~hit], clean[~hit])
+    # the smallest scales, and the largest over blocks of zeros
+    c, s = down[0].clone(), down[1].clone()
+    c.view(experts * hidden, blocks, block // 2)[hidden + at, at] = 0
+    zero = run(up, (c, s, down[2]))
+    s[hidden + at, at] = huge
+    assert torch.equal(run(up, (c, s, down[2])), zero)
+    s = down[1].clone()
+    s[hidden + at, at] = tiny
+    check_y(run(up, (down[0], s, down[2])), x, decode(up, fmt, experts), decode((down[0], s, down[2]), fmt, experts), ids, w)
+    assert fq.fp4q_device_fault() == 0
