@@ -504,8 +504,9 @@ FP4Q_API int fp4q_f8_gemm(const uint8_t* codes_a, const float* scales_a, int64_t
  *  workspace  device scratch of at least fp4q_moe_workspace_size() bytes (16-byte
  *           aligned).  Its first 64 bytes hold the counters through which the
  *           kernel's CTAs wait for one another: zero before the first call that
- *           uses the workspace, and left zero by every completed call (fill
- *           them again after a call that set the device fault word).  One
+ *           uses the workspace, and left zero by every completed call.  Where
+ *           they are not, the results are wrong and the device fault word is
+ *           set; fill them with zeros after a call that set it.  One
  *           workspace serves layers of any size; calls that share it must not
  *           run at the same time.
  * hidden and inter: multiples of 32 (128 for FP4Q_F8_BLOCK128), FP4Q_ERR_SHAPE
@@ -539,9 +540,11 @@ FP4Q_API int fp4q_moe(const void* x, int64_t tokens, int64_t hidden, int64_t int
 FP4Q_API size_t fp4q_moe_workspace_size(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k);
 
 /* The library's device fault word on the current device, read into
- * *fault_out: 0 normally; 1 once a kernel on the tensor cores (fp4q_gemm, fp4q_f8_gemm) or fp4q_moe
- * gave up a bounded wait for its copies or matrix-multiply instructions
- * instead of hanging; the outputs of that call are then incomplete.  clear != 0 resets the word to 0
+ * *fault_out: 0 normally; 1 once a kernel on the tensor cores (fp4q_gemm,
+ * fp4q_f8_gemm) or fp4q_moe gave up a bounded wait for its copies or
+ * matrix-multiply instructions instead of hanging, or fp4q_moe found the
+ * counters of its workspace in use; the outputs of that call are then
+ * incomplete or wrong.  clear != 0 resets the word to 0
  * after reading it.  The pages have no counterpart: this is the library's own
  * failure report.  Unlike every other entry point this call synchronizes the
  * current device (it reads device memory).  FP4Q_ERR_NULL if fault_out is

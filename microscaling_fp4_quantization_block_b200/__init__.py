@@ -693,8 +693,9 @@ def fp4q_moe(x: torch.Tensor, router: Optional[torch.Tensor], top_k: int, up, do
     "nvfp4", block 16) or (codes, scales) of fp4q_f8_quantize by tiles (fmt "f8"),
     for [experts * 2 inter, hidden] (gate rows, then up rows) and [experts *
     hidden, inter].  router: bf16 [experts, hidden]; None reads ids and weights
-    instead.  workspace: zero-filled, fp4q_moe_workspace_size() bytes, kept by
-    callers that call often."""
+    instead.  workspace: fp4q_moe_workspace_size() bytes, kept by callers that call
+    often; its first 64 bytes have to be zero before its first call and after one
+    that set fp4q_device_fault(), which a workspace in another state sets."""
     if x.dtype != torch.bfloat16 or x.dim() != 2:
         raise ValueError("x must be a 2-D bf16 tensor")
     fmt = fmt.lower() if isinstance(fmt, str) else fmt

@@ -1148,13 +1148,22 @@ __device__ __forceinline__ void add_slices(const Params& p, const Shared& sh, in
     }
 }
 
+// One more CTA at a counter; what it held before.  A counter that was not zero before the call lets waits pass too
+// early: one of the CTAs then finds it at `limit` (all CTAs) or above, and the fault word tells the caller.
+__device__ __forceinline__ unsigned int count(unsigned int* counter, unsigned int limit, unsigned int* fault)
+{
+    const unsigned int before = atomicAdd(counter, 1u);
+    if (before >= limit) atomicExch(fault, 1u);
+    return before;
+}
+
 // All of this CTA's summing warps have stored: count it.
-__device__ __forceinline__ void sums_count(unsigned int* counter)
+__device__ __forceinline__ void sums_count(const Params& p, unsigned int* counter)
 {
     sums_sync();
     if (threadIdx.x == 32 * FIRST_SUM) {
         __threadfence();
-        atomicAdd(counter, 1u);
+        count(counter, gridDim.x, p.fault);
     }
 }
 
@@ -1164,7 +1173,7 @@ __device__ __forceinline__ void all_ctas(const Params& p, unsigned int n)
     __syncthreads();
     if (threadIdx.x == 0) {
         __threadfence();
-        atomicAdd(&p.ctl->start, 1u);
+        count(&p.ctl->start, n * gridDim.x, p.fault);
         spin(&p.ctl->start, n * gridDim.x, p.fault);
     }
     __syncthreads();
@@ -1241,12 +1250,12 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(const __grid_constant__
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHERS));
         bool live = true;
         add_slices<FMT, 0>(p, sh, stream, buf, live);
-        sums_count(&p.ctl->h_done);
+        sums_count(p, &p.ctl->h_done);
         // the pairs' maxima are read directly, not through a stage
         if (threadIdx.x == 32 * FIRST_SUM) spin(&p.ctl->h_done, gridDim.x, p.fault);
         sums_sync();
         add_slices<FMT, 1>(p, sh, stream, buf, live);
-        sums_count(&p.ctl->o_done);
+        sums_count(p, &p.ctl->o_done);
     }
     __syncthreads();
     if (threadIdx.x == 0) spin(&p.ctl->o_done, gridDim.x, p.fault);
@@ -1273,7 +1282,7 @@ __global__ void __launch_bounds__(THREADS, 1) moe_kernel(const __grid_constant__
     }
     if (threadIdx.x == 0) {
         // the last CTA to get here leaves the counters as it found them
-        if (atomicAdd(&p.ctl->leaving, 1u) == gridDim.x - 1) {
+        if (count(&p.ctl->leaving, gridDim.x, p.fault) == gridDim.x - 1) {
             p.ctl->start = p.ctl->h_done = p.ctl->o_done = 0u;
             __threadfence();
             p.ctl->leaving = 0u;

@@ -517,3 +517,25 @@ def test_scale_bytes_at_the_ends(fq, fmt, nan, tiny, huge, tokens):
     s[hidden + at, at] = tiny
     check_y(run(up, (down[0], s, down[2])), x, decode(up, fmt, experts), decode((down[0], s, down[2]), fmt, experts), ids, w)
     assert fq.fp4q_device_fault() == 0
+
+
+@pytest.mark.parametrize("counter,value", [(0, 1), (0, 5), (0, 2 ** 31 - 1), (1, 3), (1, 1000), (2, 1), (2, 1000), (3, 1000)])
+@pytest.mark.parametrize("tokens", [2, 20])
+def test_a_workspace_in_use_is_reported(fq, counter, value, tokens):
+    """Counters that were not zero let waits pass early (all accesses stay within bounds): the fault word tells, and
+    a workspace filled with zeros serves again."""
+    experts, top_k, hidden, inter = 6, 2, 256, 128
+    up = experts_of(fq, "nvfp4", experts, 2 * inter, hidden, 0.06, 1)
+    down = experts_of(fq, "nvfp4", experts, hidden, inter, 0.09, 2)
+    router = workloads.gaussian_bf16(experts, hidden, 0.06, 4, device="cuda")
+    x = workloads.gaussian_bf16(tokens, hidden, 1.0, 3, device="cuda")
+    want = fq.fp4q_moe(x, router, top_k, up, down, "nvfp4")
+    ws = torch.zeros((fq.fp4q_moe_workspace_size(tokens, hidden, inter, experts, top_k),), dtype=torch.uint8, device="cuda")
+    ws[:16].view(torch.int32)[counter] = value
+    assert fq.fp4q_device_fault() == 0
+    fq.fp4q_moe(x, router, top_k, up, down, "nvfp4", workspace=ws)
+    assert fq.fp4q_device_fault(clear=True) == 1
+    ws[:64].zero_()
+    got = fq.fp4q_moe(x, router, top_k, up, down, "nvfp4", workspace=ws)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert fq.fp4q_device_fault() == 0 and not ws[:64].any()
