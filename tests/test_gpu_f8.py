@@ -278,3 +278,60 @@ def test_past_32_bits(fq):
     wc, ws = quantize_oracle(y[m // 128 * 128:].cpu(), TILE)
     assert same(c[m // 128 * 128:], wc) and same(s[-1:], ws)
     assert fq.fp4q_device_fault() == 0
+
+
+# ------------------------------------------------------------------ the product, every kernel and split
+# What the choice in fp4q_f8_gemm makes of them, by m, n and k:
+EVERY = [
+    # tiles of 128 x 256, many blocks of k and a short last one: n odd, a multiple of 16 alone; two and more tiles a CTA
+    (700, 4001, 2064), (700, 4112, 2064), (2500, 3001, 2064), (1100, 2999, 4112),
+    # tiles of 128 x 128, likewise; SMs without a tile
+    (1300, 7000, 1040), (1000, 1000, 2320), (200, 3584, 4880),
+    # 17 to 32 rows, alone and over clusters of 8; more CTAs because the scales do not fit one; not even in eight
+    (17, 257, 112), (24, 1000, 2064), (31, 131, 5136), (32, 20000, 1040), (25, 20000, 14608), (20, 130, 115856),
+    # up to 16 and up to 64 rows: the same two
+    (5, 20000, 26256), (3, 40, 209056), (40, 20000, 6160), (64, 19100, 11920), (64, 130, 46224), (33, 301, 46224),
+    # more than 64 rows in tiles of 64 over clusters
+    (130, 130, 9232), (300, 300, 9232),
+]
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("m,n,k", EVERY)
+def test_gemm_every_kernel_on_integers(fq, m, n, k, out):
+    """Integers up to 8 under scales of 1/2 to 2: multiples of 1/4 below 2^20, so every fp32 sum in any order is exact
+    and the result is the exact one rounded once."""
+    g = torch.Generator(device="cuda").manual_seed(m + n + k)
+    a = torch.randint(-8, 9, (m, k), generator=g, device="cuda").float()
+    b = torch.randint(-8, 9, (n, k), generator=g, device="cuda").float()
+    kb = -(-k // 128)
+    sa = torch.exp2(torch.randint(-1, 2, (m, kb), generator=g, device="cuda").float())
+    sb = torch.exp2(torch.randint(-1, 2, (-(-n // 128), kb), generator=g, device="cuda").float())
+    guard = torch.full((m + 2, n), 7.0, dtype=out, device="cuda")
+    y = fq.fp4q_f8_gemm(a.to(torch.float8_e4m3fn), sa, b.to(torch.float8_e4m3fn), sb, out, y=guard[1:m + 1])
+    A = a.double() * sa.double().repeat_interleave(128, 1)[:, :k]
+    B = b.double() * sb.double().repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)[:, :k]
+    want = A @ B.T
+    assert float(want.abs().max()) < 2.0 ** 20
+    assert torch.equal(y, want.to(out))
+    assert bool((guard[0] == 7.0).all()) and bool((guard[m + 1] == 7.0).all())
+    assert fq.fp4q_device_fault() == 0
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("m,n,k", EVERY)
+def test_gemm_every_kernel_against_64_bits(fq, m, n, k, out):
+    """Operands as the quantizer makes them, the bar of the product at the top; on the GPU."""
+    x, _ = workloads.student_t_outliers_bf16(m, k, seed=m + k, n_outlier=8, device="cuda")
+    w = workloads.gaussian_bf16(n, k, 0.02, seed=n + k, device="cuda")
+    a, sa = fq.fp4q_f8_quantize(x, ROW)
+    b, sb = fq.fp4q_f8_quantize(w, TILE)
+    y = fq.fp4q_f8_gemm(a, sa, b, sb, out)
+    A = a.double() * sa.double().repeat_interleave(128, 1)[:, :k]
+    B = b.double() * sb.double().repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)[:, :k]
+    want, mag = A @ B.T, A.abs() @ B.abs().T
+    u = torch.finfo(out).eps / 2
+    tol = (17 + sa.shape[1]) * 2.0 ** -24 * mag * (1 + u) + u * want.abs()
+    err = (y.double() - want).abs()
+    assert bool((err <= tol).all()), float((err / tol.clamp(min=1e-300)).max())
+    assert fq.fp4q_device_fault() == 0
