@@ -539,3 +539,122 @@ def test_a_workspace_in_use_is_reported(fq, counter, value, tokens):
     got = fq.fp4q_moe(x, router, top_k, up, down, "nvfp4", workspace=ws)
     assert all(torch.equal(a, b) for a, b in zip(want, got))
     assert fq.fp4q_device_fault() == 0 and not ws[:64].any()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4", "f8"])
+def test_rows_of_every_size(fq, fmt):
+    """Rows of x from 2^-60 to 2^60: a row's values are kept under its own power of two."""
+    tokens, experts, hidden, inter = 25, 3, 256, 128
+    up = experts_of(fq, fmt, experts, 2 * inter, hidden, 0.02, 1)
+    down = experts_of(fq, fmt, experts, hidden, inter, 0.05, 2)
+    x = workloads.gaussian_bf16(tokens, hidden, 1.0, 3).float() * torch.exp2(torch.linspace(-60, 60, tokens))[:, None]
+    x = x.bfloat16().cuda()
+    ids = torch.arange(tokens * 2, dtype=torch.int32).view(tokens, 2) % experts
+    w = torch.full((tokens, 2), 0.5)
+    y, _, _ = fq.fp4q_moe(x, None, 2, up, down, fmt, ids=ids.cuda(), weights=w.cuda())
+    want, tol = layer64(x, decode(up, fmt, experts), decode(down, fmt, experts), ids, w)
+    assert bool(torch.isfinite(y).all()) and float(want.abs().max()) > 2.0 ** 110
+    # products of powers far below the smallest normal fp32 value are not held: 2^-126 per value of h
+    tol += 2.0 ** -120
+    err = (y.cpu().double() - want).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4", "f8"])
+def test_channels_far_above_the_rest(fq, fmt):
+    """One channel of each token 2^12 to 2^30 above the others, and no weight on it: the small values decide the
+    result, exact as long as they lie above 2^-24 of the row's largest, off by 2^-32 of it at most below."""
+    tokens, experts, hidden, inter = 19, 3, 512, 128
+    at = torch.arange(tokens) * 27 + 3
+    w = workloads.gaussian_bf16(experts * 2 * inter, hidden, 0.05, 1, device="cuda")
+    w[:, at.cuda()] = 0.0
+    if fmt == "f8":
+        up = fq.fp4q_f8_quantize(w, "tile")
+    else:
+        up = fq.fp4q_quantize(w, fmt, 32 if fmt == "mxfp4" else 16, 0, "none" if fmt == "mxfp4" else "compute")
+    down = experts_of(fq, fmt, experts, hidden, inter, 0.05, 2)
+    x = workloads.gaussian_bf16(tokens, hidden, 1.0, 3)
+    power = torch.arange(tokens) + 12
+    x[torch.arange(tokens), at] = torch.exp2(power.float()).bfloat16()
+    x = x.cuda()
+    ids = torch.arange(tokens * 2, dtype=torch.int32).view(tokens, 2) % experts
+    wt = torch.full((tokens, 2), 0.5)
+    y, _, _ = fq.fp4q_moe(x, None, 2, up, down, fmt, ids=ids.cuda(), weights=wt.cuda())
+    U64, D64 = decode(up, fmt, experts), decode(down, fmt, experts)
+    assert not U64[:, :, at].any()
+    want, tol = layer64(x, U64, D64, ids, wt)
+    err = (y.cpu().double() - want).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+    exact = power <= 16                                      # values down to 2^-8 of one keep their eight bits
+    assert float(err[exact].norm()) <= 2.0 ** -8 * float(want[exact].norm())
+
+
+def test_nvfp4_without_a_tensor_scale(fq):
+    """NVFP4 operands quantized without a per-tensor scale, on either side or both."""
+    tokens, experts, top_k, hidden, inter = 21, 5, 2, 544, 96
+    router = workloads.gaussian_bf16(experts, hidden, 0.05, 3, device="cuda")
+    x = workloads.gaussian_bf16(tokens, hidden, 1.0, 4, device="cuda")
+    plain = [fq.fp4q_quantize(workloads.gaussian_bf16(experts * r, c, s, 5 + r, device="cuda"), "nvfp4", 16)
+             for r, c, s in ((2 * inter, hidden, 0.05), (hidden, inter, 0.08))]
+    scaled = [experts_of(fq, "nvfp4", experts, 2 * inter, hidden, 0.05, 6, per_expert=True),
+              experts_of(fq, "nvfp4", experts, hidden, inter, 0.08, 7)]
+    assert plain[0][2] is None and plain[1][2] is None
+    for up, down in ((plain[0], plain[1]), (plain[0], scaled[1]), (scaled[0], plain[1][:2])):
+        y, ids, w = fq.fp4q_moe(x, router, top_k, up, down, "nvfp4")
+        check_route(ids, w, x, router, top_k, True)
+        check_y(y, x, decode(up, "nvfp4", experts), decode(down, "nvfp4", experts), ids, w)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4", "f8"])
+def test_a_wide_layer_of_many_experts(fq, fmt):
+    """256 experts of 7168 x 2048 and 512 pairs, each expert's matrices decoded to 64 bits on the GPU; the bars of the top."""
+    tokens, experts, top_k, hidden, inter = 64, 256, 8, 7168, 2048
+    g = torch.Generator(device="cuda").manual_seed(8)
+
+    def matrix(rows, cols):
+        draw = lambda lo, hi, *shape: torch.randint(lo, hi, shape, generator=g, device="cuda", dtype=torch.uint8)
+        if fmt == "f8":                                      # codes of 1/16 to 15, either sign
+            codes = draw(0x18, 0x58, experts * rows, cols) | draw(0, 2, experts * rows, 1) << 7
+            scales = torch.rand((experts * rows // 128, cols // 128), generator=g, device="cuda") * (0.2 / cols ** 0.5)
+            return codes.view(torch.float8_e4m3fn), scales
+        codes = draw(0, 256, experts * rows, cols // 2)
+        if fmt == "mxfp4":
+            return codes, draw(118, 121, experts * rows, cols // 32), None
+        return codes, draw(0x28, 0x39, experts * rows, cols // 16), torch.rand((experts,), generator=g, device="cuda") * (0.7 / cols ** 0.5)
+
+    grid = torch.cat((GRID, -GRID)).cuda()
+
+    def expert(m, e, rows):
+        c, s = m[0][e * rows:(e + 1) * rows], m[1].view(experts, -1, m[1].shape[1])[e].double()
+        if fmt == "f8":
+            return c.double() * s.repeat_interleave(128, 0).repeat_interleave(128, 1)
+        v = torch.stack((grid[(c & 15).long()], grid[(c >> 4).long()]), -1).view(rows, -1)
+        s = torch.exp2(s - 127) if fmt == "mxfp4" else m[1].view(experts, rows, -1)[e].view(torch.float8_e4m3fn).double() * m[2][e].double()
+        return v * s.repeat_interleave(v.shape[1] // s.shape[1], 1)
+
+    up, down = matrix(2 * inter, hidden), matrix(hidden, inter)
+    router = workloads.gaussian_bf16(experts, hidden, hidden ** -0.5, 3, device="cuda")
+    x = workloads.gaussian_bf16(tokens, hidden, 1.0 if fmt != "mxfp4" else 0.5, 4, device="cuda")
+    y, ids, w = fq.fp4q_moe(x, router, top_k, up, down, fmt)
+    assert fq.fp4q_device_fault() == 0
+    check_route(ids, w, x, router, top_k, True)
+    xd, want = x.double(), torch.zeros((tokens, hidden), dtype=torch.float64, device="cuda")
+    far = torch.zeros_like(want)
+    for e in range(experts):
+        token, slot = torch.nonzero(ids == e, as_tuple=True)
+        if not token.numel():
+            continue
+        xe, W, D, we = xd[token], expert(up, e, 2 * inter), expert(down, e, hidden), w.double()[token, slot][:, None]
+        v = xe @ W.T
+        ev = (hidden / 64 + 24) * U * (xe.abs() @ W.abs().T) + 2.0 ** -32 * top_of(xe) * W.abs().sum(1)
+        gate, u, eg, eu = v[:, :inter], v[:, inter:], ev[:, :inter], ev[:, inter:]
+        silu = gate * torch.sigmoid(gate)
+        h = silu * u
+        eh = 1.1 * eg * (u.abs() + eu) + silu.abs() * eu + (2.0 ** -11 + 2.0 ** -20) * h.abs() + 2.0 ** -24 * top_of(h)
+        want.index_add_(0, token, (h @ D.T) * we)
+        far.index_add_(0, token, (eh @ D.abs().T + (inter / 64 + 24 + top_k) * U * ((h.abs() + eh) @ D.abs().T)) * we)
+    half = torch.finfo(torch.bfloat16).eps / 2
+    err, tol = (y.double() - want).abs(), far * (1 + half) + half * want.abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+    assert float(err.norm()) <= 2.0 ** -8 * float(want.norm())
+    assert len(set(ids.flatten().tolist())) > 180
