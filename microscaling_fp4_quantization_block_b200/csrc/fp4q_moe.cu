@@ -771,12 +771,9 @@ __device__ __forceinline__ void widen8(uint32_t lo, uint32_t hi, uint32_t (&h)[4
         : "r"(lo), "r"(hi));
 }
 
-// Two UE4M3 bytes as f16.  The bytes from 0x7F on are NaN, as in ue4m3_decode: the conversion takes
-// a byte's top bit for a sign, so the bits below it are set.
+// Two UE4M3 bytes as f16; the conversion takes a byte's top bit for a sign (see the end of item).
 __device__ __forceinline__ uint32_t ue4m3_pair(uint32_t c)
 {
-    const uint32_t top = c & 0x8080u;
-    c |= top - (top >> 7);
     uint32_t h;
     asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(c));
     return h;
@@ -850,6 +847,7 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
                 scale_at[i][r] = (32u * i + row) * F::SCALE_PITCH + (((uint32_t)(row0 + i * f.second) + row) * (uint32_t)srb & 15u);
             }
     }
+    uint32_t seen[2][2] = {};                                // NVFP4: the scale bytes of this lane's rows, or'ed
     int col[NT];                                             // columns past the last pair repeat it
 #pragma unroll
     for (int c = 0; c < NT; ++c) col[c] = min(8 * c + g, n - 1);
@@ -953,7 +951,10 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) two[i][r] = lds16(aux + scale_at[i][r] + 2u * (4 * qi + t));
+                        for (int r = 0; r < 2; ++r) {
+                            two[i][r] = t < left ? lds16(aux + scale_at[i][r] + 2u * (4 * qi + t)) : 0u;   // past the row: zeros
+                            seen[i][r] |= two[i][r];
+                        }
                 }
 #pragma unroll
                 for (int c = 0; c < NT; ++c) {
@@ -980,8 +981,8 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
                             const uint32_t h = ue4m3_pair(two[i][r]);
-                            m[r][0] = t < left ? __byte_perm(h, h, 0x1010) : 0u;     // past the row: zeros times zeros
-                            m[r][1] = t < left ? __byte_perm(h, h, 0x3232) : 0u;
+                            m[r][0] = __byte_perm(h, h, 0x1010);
+                            m[r][1] = __byte_perm(h, h, 0x3232);
                         }
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -1029,6 +1030,26 @@ __device__ __forceinline__ void item(const Params& p, const Plan& q, uint32_t ri
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(empty0 + 8u * s);
+    }
+    if constexpr (FMT == kNv) {
+        // A byte from 0x80 on is NaN (ue4m3_decode), and was taken for a negative scale: its row's sums become NaN
+        // here, once an item (64 tokens over the wide layer 314 us; each byte turned into NaN on its way, 316).
+        uint32_t flags = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) flags |= (seen[i][r] & 0x8080u) ? 1u << (2 * i + r) : 0u;
+        if (__any_sync(0xffffffffu, flags != 0u)) {
+            flags |= __shfl_xor_sync(0xffffffffu, flags, 1);             // the four lanes that share rows
+            flags |= __shfl_xor_sync(0xffffffffu, flags, 2);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int c = 0; c < NT; ++c)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (flags >> (2 * i + (j >> 1)) & 1u) acc[i][c][j] = as_f32(0x7fc00000u);
+        }
     }
 }
 
