@@ -464,8 +464,9 @@ FP4Q_API int fp4q_f8_quantize(const void* x, int64_t rows, int64_t cols, int gra
  * blocks of 128 along k.  A is m x k quantized by rows, B is n x k quantized by
  * tiles (a linear layer's [out][in] weights).  The products are exact; a
  * block's sum is accumulated in fp32 in the tensor cores, then fp32(sA sB)
- * times it is added to an fp32 running sum by one fused multiply-add, and the
- * result is rounded once.
+ * times it is added to an fp32 running sum by one fused multiply-add (for few
+ * rows of A: to one of up to eight, each over a part of k, which are added in
+ * order at the end), and the result is rounded once.
  *  codes_a, codes_b   [rows][k] E4M3, 16-byte aligned; k a multiple of 16
  *          (FP4Q_ERR_SHAPE otherwise); m, n any, each below 2^31 - 256.
  *  scales_a  [m][ceil(k / 128)]; scales_b  [ceil(n / 128)][ceil(k / 128)].
@@ -478,7 +479,8 @@ FP4Q_API int fp4q_f8_gemm(const uint8_t* codes_a, const float* scales_a, int64_t
 /*
  * fp4q_moe -- a whole mixture-of-experts layer for a few tokens (decoding):
  * router, the chosen experts' gated MLPs over quantized weights, and the
- * weighted sum, in one kernel that reads each chosen expert's weights once
+ * weighted sum, in one kernel that reads a chosen expert's weights once for
+ * every 16 tokens that chose it
  * ("Diagnosing FP4 inference", Methodology: weights in FP4, dequantized for the
  * compute; the activations stay in 16 bits):
  *   l = x router^T;  the top_k largest logits of each token (equal logits: the
@@ -500,6 +502,7 @@ FP4Q_API int fp4q_f8_gemm(const uint8_t* codes_a, const float* scales_a, int64_t
  *           of experts * rows rows, or quantized expert by expert.
  *           gscale: the per-tensor scale of NVFP4, one for all experts
  *           (gscale_stride 0) or one each (1), or NULL for 1; NULL otherwise.
+ *           (After FROM_AMAX it is the second of the two floats.)
  *  y        bf16 [tokens][hidden], overwritten.
  *  workspace  device scratch of at least fp4q_moe_workspace_size() bytes (16-byte
  *           aligned).  Its first 64 bytes hold the counters through which the
@@ -513,8 +516,11 @@ FP4Q_API int fp4q_f8_gemm(const uint8_t* codes_a, const float* scales_a, int64_t
  * otherwise, at most 65536; experts, top_k at most FP4Q_MOE_MAX_EXPERTS,
  * FP4Q_MOE_MAX_TOPK and top_k at most experts: FP4Q_ERR_UNSUPPORTED.  x, y,
  * router, codes, scales 16-byte aligned.  Logits are 64-bit sums; inside the
- * products x is exact to 2^-25 of the largest of each 32 values, h has 11
- * significant bits, sums are fp32 in a fixed order, and y is rounded once.
+ * products x keeps every bit of the values down to 2^-24 of its row's largest
+ * and is off by at most 2^-32 of that largest below, h has 11 significant bits
+ * down to 2^-21 of its row's largest and is off by at most 2^-24 of it below,
+ * sums are fp32 in a fixed order, and y is rounded once.  A token's results do
+ * not depend on the other tokens of the call.
  * Scale bytes that are NaN (E8M0 255; UE4M3 from 0x7F on) make every result
  * that takes them NaN.  The sums are formed before G and the power of two that
  * a row of x or h is kept under: weights (codes times scales) whose magnitudes

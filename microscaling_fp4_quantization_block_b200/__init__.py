@@ -692,7 +692,7 @@ def fp4q_moe(x: torch.Tensor, router: Optional[torch.Tensor], top_k: int, up, do
     up, down: (codes, scales, gscale) of fp4q_quantize (fmt "mxfp4", block 32, or
     "nvfp4", block 16) or (codes, scales) of fp4q_f8_quantize by tiles (fmt "f8"),
     for [experts * 2 inter, hidden] (gate rows, then up rows) and [experts *
-    hidden, inter].  router: bf16 [experts, hidden]; None reads ids and weights
+    hidden, inter]; gscale 1 or experts floats (of from_amax's two the second).  router: bf16 [experts, hidden]; None reads ids and weights
     instead.  workspace: fp4q_moe_workspace_size() bytes, kept by callers that call
     often; its first 64 bytes have to be zero before its first call and after one
     that set fp4q_device_fault(), which a workspace in another state sets."""

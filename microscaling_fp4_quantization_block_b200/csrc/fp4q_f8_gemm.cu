@@ -21,10 +21,12 @@
 // Every wait is bounded; a wait that runs out records the library's fault word
 // and the CTA stops its work and returns.
 //
-// Measured (graph replays): 8192 x 13824 x 5120 567 us, 2.05 PFLOP/s (0.62 of
-// twice the measured bf16 rate; 490 us with the accumulators left unread); 1 x
-// 13824 x 5120 18.8 us (its bytes at the copy rate: 10.8); 37 x 3584 x 18944 20.8
-// (10.5).
+// Measured, in a loop of calls: 8192 x 13824 x 5120 658 us under the power cap,
+// 1.76 PFLOP/s (0.53 of twice the measured bf16 rate); in graph replays on a cool
+// chip 566, of 351 at that rate, and 490 with the accumulators left unread: the
+// operands' way from L2 costs 139 us over the floor, the sums' way out of tensor
+// memory 76.  1 x 13824 x 5120 15.7 us (its bytes at the copy rate: 10.8); 37 x
+// 3584 x 18944 17.9 (10.5).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -662,7 +664,10 @@ extern "C" int fp4q_f8_gemm(const uint8_t* codes_a, const float* scales_a, int64
     // Which kernel, by the times measured on 12 shapes (n 3584 to 13824, k 5120 and 18944, m 100 to 1024): a tile of
     // 128 x 256 takes 0.59 us a block of k, one of 128 x 128 0.32, both after 3 us; a CTA of the few-token kernel 0.38
     // after 10.  Up to 64 rows B's bytes bound the product and the few-token kernel, with all SMs, always leads
-    // (37 x 3584 x 18944: 21 against 67 us); at 200 x 5120 x 5120 it takes 26 us, tiles of 128 x 128 take 16.
+    // (37 x 3584 x 18944: 18 against 67 us); at 256 x 5120 x 5120 it takes 24.8 us, tiles of 128 x 128 take 15.8.
+    // That holds within 10 % where the rows begin on 128-byte lines and y takes whole stores (200 x 3584 x 18944: 50
+    // by the rule, 46 measured; 777 x 1024 x 4096: 13.2 and 13.1); an odd n adds 2 us there, k = 4112 another 3, so
+    // that 777 x 1001 x 4112 takes 18.5 us where the rule says 13.6 and the few-token kernel would take 17.1.
     const int64_t tiles_m = (m + 127) / 128;
     const int64_t waves128 = (tiles_m * ((n + 127) / 128) + 147) / 148, waves256 = (tiles_m * ((n + 255) / 256) + 147) / 148;
     const int64_t ns128 = 3000 + 320 * p.kb * waves128, ns256 = 3000 + 590 * p.kb * waves256;

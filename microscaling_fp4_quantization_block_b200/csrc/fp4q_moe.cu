@@ -5,10 +5,11 @@
 //   y   = sum over a token's pairs of w_p D_e h_p.
 //
 // With few tokens the layer is bound by the chosen experts' quantized weights,
-// each read once, so everything else is arranged around one stream of them:
+// so everything else is arranged around one stream of them:
 // one CTA per SM walks a static share of (group, 64-row tile) items, a group
-// being up to 16 pairs of one expert, first of the gate/up matrices (32 rows
-// of each), then of the down matrices, two items at a time.  Each of the two
+// being up to 16 pairs of one expert (for which its weights are read once), first
+// of the gate/up matrices (32 rows of each), then of the down matrices, two items
+// at a time.  Each of the two
 // streams has half of a ring of shared-memory stages and, of the CTA's warps,
 //   one (16, 18) that fetches the items' weight rows (TMA tiles of 32 rows x 128
 //     bytes, 128-byte swizzle), ahead of the layer's dependencies: the first
@@ -22,20 +23,22 @@
 //   two (20 and 21, 22 and 23) that add the four slices of k and finish the item
 //     (silu, h; or the pairs' results) while the next one is multiplied.
 // The weights are widened to fp16 in registers on their way from shared memory
-// into the product; tcgen05.mma, whose operands lie in shared or tensor memory,
-// would need them written back first: 2 bytes a weight through shared memory,
-// four times what the codes cost it.  mma.sync reaches 690 multiply-adds a clock
+// into the product.  tcgen05.mma takes its operands from shared or tensor memory:
+// written back to shared memory the weights would cost it four times what the
+// codes do; as an operand in tensor memory (tcgen05.st) they would not, a form
+// that has not been built.  mma.sync reaches 690 multiply-adds a clock
 // and SM here, 15 columns' worth at the rate HBM delivers FP4 weights, so groups
 // of more than 8 pairs are near its bound.
 //
-// Measured (graph replays; the experts' bytes at the copy rate of 6.55 TB/s in
-// brackets): 1 token, 8 of 64 NVFP4 experts of 2048 x 1024, 28 us (4.4): launch,
+// Measured (a loop of calls; the experts' bytes at the copy rate of 6.55 TB/s in
+// brackets): 1 token, 8 of 64 NVFP4 experts of 2048 x 1024, 29 us (4.4): launch,
 // router, choices and the three waits take 17 of them; 5 tokens over E4M3 experts
 // 55 us (26); 23 tokens over 60 NVFP4 experts 62 us (24); 64 tokens over 128 MXFP4
-// experts of 2048 x 768 127 us (48); over 64 NVFP4 experts of 5120 x 1792 299 us
-// (152).  With the products left out these take 25, 51, 51, 95 and 215 us: what
-// bounds the long calls is the products' instructions on top of a stream of 4 to
-// 5 TB/s that the warps filling the stages sustain.
+// experts of 2048 x 768 127 us (48); over 64 NVFP4 experts of 5120 x 1792 314 us
+// (152).  An earlier build took 28, 55, 62, 127 and 299, and without its products
+// 25, 51, 51, 95 and 215: what bounds the long calls is the products' instructions
+// on top of the stream that the warps filling the stages sustain, and that stream
+// carries, beside the weights, a group's activations again for every item.
 //
 // Activations enter the products as fp16 under one power of two per row (the
 // row's largest value in [2^7, 2^8)): bf16 inputs keep every bit down to 2^-24
@@ -47,7 +50,7 @@
 // multiply the fp32 sums of their blocks.
 //
 // Sums across k are in a fixed order and a token's pairs are added in slot
-// order, so results do not depend on timing.  The points where all CTAs
+// order, so results depend neither on timing nor on the call's other tokens.  The points where all CTAs
 // wait for one another (x and logits, choices, h, pair results) count
 // in the workspace; the launch is cooperative, so all CTAs are resident, and
 // every wait is bounded: one that runs out records the library's fault word
