@@ -174,7 +174,8 @@ def fp4q_status_string(status: int) -> str:
 
 def fp4q_device_fault(clear: bool = False) -> int:
     """The library's device fault word on the current device (0, or 1 after a
-    tensor-core kernel gave up a bounded wait); synchronizes the device."""
+    tensor-core kernel or fp4q_moe gave up a bounded wait, or fp4q_moe found its
+    workspace in use); synchronizes the device."""
     out = ctypes.c_uint(0)
     _check(lib().fp4q_device_fault(ctypes.addressof(out), int(bool(clear))), "fp4q_device_fault")
     return int(out.value)

@@ -658,3 +658,63 @@ def test_a_wide_layer_of_many_experts(fq, fmt):
     assert bool((err <= tol).all()), float((err / tol).max())
     assert float(err.norm()) <= 2.0 ** -8 * float(want.norm())
     assert len(set(ids.flatten().tolist())) > 180
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4", "f8"])
+@pytest.mark.parametrize("tokens,experts,top_k,hidden,inter", [
+    (3, 2, 1, 65536, 128), (3, 2, 2, 128, 65536), (5, 2, 2, 65408, 256), (64, 512, 16, 128, 128), (1, 1, 1, 128, 128)])
+def test_sizes_at_the_limits(fq, fmt, tokens, experts, top_k, hidden, inter):
+    """The longest rows, the most experts and choices, one of each; memory beside the results and the workspace kept."""
+    up = experts_of(fq, fmt, experts, 2 * inter, hidden, hidden ** -0.5, 1)
+    down = experts_of(fq, fmt, experts, hidden, inter, inter ** -0.5, 2)
+    x = workloads.gaussian_bf16(tokens, hidden, 1.0, 3, device="cuda")
+    router = workloads.gaussian_bf16(experts, hidden, hidden ** -0.5, 4, device="cuda")
+    size = fq.fp4q_moe_workspace_size(tokens, hidden, inter, experts, top_k)
+    ws = torch.zeros((size + 64,), dtype=torch.uint8, device="cuda")
+    ws[size:] = 0xAB
+    guard = torch.full((tokens + 2, hidden), 5.0, dtype=torch.bfloat16, device="cuda")
+    y, ids, w = fq.fp4q_moe(x, router, top_k, up, down, fmt, False, workspace=ws[:size], y=guard[1:tokens + 1])
+    assert fq.fp4q_device_fault() == 0
+    assert bool((ws[size:] == 0xAB).all()) and bool((guard[0] == 5.0).all()) and bool((guard[-1] == 5.0).all())
+    check_route(ids, w, x, router, top_k, False)
+    check_y(y, x, decode(up, fmt, experts), decode(down, fmt, experts), ids, w)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4", "f8"])
+def test_every_choice_on_one_expert(fq, fmt):
+    """1024 pairs, 64 groups, of one expert among 20."""
+    tokens, experts, top_k, hidden, inter = 64, 20, 16, 256, 384
+    up = experts_of(fq, fmt, experts, 2 * inter, hidden, 0.05, 1)
+    down = experts_of(fq, fmt, experts, hidden, inter, 0.05, 2)
+    x = workloads.gaussian_bf16(tokens, hidden, 1.0, 3, device="cuda")
+    ids = torch.full((tokens, top_k), 19, dtype=torch.int32)
+    w = torch.rand((tokens, top_k), generator=torch.Generator().manual_seed(4))
+    y, _, _ = fq.fp4q_moe(x, None, top_k, up, down, fmt, ids=ids.cuda(), weights=w.cuda())
+    assert fq.fp4q_device_fault() == 0
+    check_y(y, x, decode(up, fmt, experts), decode(down, fmt, experts), ids, w)
+
+
+def test_a_run_of_the_operators_captured(fq):
+    """Quantizer, product, layer, quantizer and product twice over in one graph, replayed on new inputs."""
+    tokens, hidden, inter, experts = 24, 512, 256, 8
+    b, sb = fq.fp4q_f8_quantize(workloads.gaussian_bf16(hidden, hidden, hidden ** -0.5, 2, device="cuda"), "tile")
+    up = experts_of(fq, "f8", experts, 2 * inter, hidden, hidden ** -0.5, 3)
+    down = experts_of(fq, "f8", experts, hidden, inter, inter ** -0.5, 4)
+    router = workloads.gaussian_bf16(experts, hidden, 0.05, 5, device="cuda")
+
+    def chain(x):
+        m = fq.fp4q_f8_gemm(*fq.fp4q_f8_quantize(x), b, sb)
+        y, _, _ = fq.fp4q_moe(m, router, 2, up, down, "f8")
+        return fq.fp4q_f8_gemm(*fq.fp4q_f8_quantize(y), b, sb)
+
+    x = workloads.gaussian_bf16(tokens, hidden, 1.0, 1, device="cuda")
+    chain(x)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = chain(chain(x))
+    for seed in (6, 7, 8):
+        new = workloads.gaussian_bf16(tokens, hidden, 1.0, seed, device="cuda")
+        x.copy_(new)
+        graph.replay()
+        assert torch.equal(out, chain(chain(new)))
+    assert fq.fp4q_device_fault() == 0
