@@ -35,10 +35,10 @@
 // router, choices and the three waits take 17 of them; 5 tokens over E4M3 experts
 // 55 us (26); 23 tokens over 60 NVFP4 experts 62 us (24); 64 tokens over 128 MXFP4
 // experts of 2048 x 768 127 us (48); over 64 NVFP4 experts of 5120 x 1792 314 us
-// (152).  An earlier build took 28, 55, 62, 127 and 299, and without its products
-// 25, 51, 51, 95 and 215: what bounds the long calls is the products' instructions
-// on top of the stream that the warps filling the stages sustain, and that stream
-// carries, beside the weights, a group's activations again for every item.
+// (152).  With logits in fp32 these took 28, 55, 62, 127 and 299, and then without
+// the products 25, 51, 51, 95 and 215: what bounds the long calls is the products'
+// instructions on top of the stream that the warps filling the stages sustain, and
+// that stream carries, beside the weights, a group's activations for every item.
 //
 // Activations enter the products as fp16 under one power of two per row (the
 // row's largest value in [2^7, 2^8)): bf16 inputs keep every bit down to 2^-24
